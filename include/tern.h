@@ -423,6 +423,141 @@ tern_status tern_debug_s8_acc(const int8_t* q, int T, const tern_weights* W, int
 tern_status tern_stream_read(const void* buf, size_t bytes, int depth, int waves_per_cu,
                              uint32_t* sink, void* stream);
 
+/* ---- Decoder operators around the projections: the RMS norm that feeds them,
+ * the 8-bit paged key/value cache and the attention over it. ---- */
+
+typedef enum { TERN_F32 = 0, TERN_BF16 = 1 } tern_dtype;
+
+/*
+ * RMS norm with the residual's addition and 8-bit output (device, async). Per token t:
+ *   h = x[t] + residual[t] in fp32, rounded to the residual's type and written
+ *       to residual_out[t] (without a residual, h = x[t]);
+ *   rho = 1 / sqrt(sum_k h[k]^2 / K + eps);  v[k] = fl(h[k] weight[k]);
+ *   y[t][k] = bf16(v[k] rho);
+ *   a = fl(max_k |v[k]| / 127);  q[t][k] = clamp(round-half-even(fl(v[k] / a)), -127, 127);
+ *   act_scale[t] = fl(rho a); a token of zeros gives scale 0 and zero codes.
+ * rho cancels in the quotient, so the codes are exact functions of v. q and
+ * act_scale (both or neither) are what tern_linear_s8_q takes; y (or NULL) is
+ * what tern_linear takes; at least one of q and y is asked for.
+ * x: [T] rows of K, x_stride elements apart, of x_type. residual and
+ * residual_out (both NULL or neither; the same buffer or disjoint ones): rows
+ * residual_stride and residual_out_stride apart, of residual_type. weight: [K]
+ * of weight_type. y: rows y_stride apart. q: [T][K] in `layout`.
+ * K a multiple of 16 (of 64 for TERN_Q_OPERAND_ORDER) up to 32768; pointers
+ * 16-byte aligned, rows too. eps >= 0. 1 <= T <= 2^19.
+ * Errors: TERN_ERR_NULL, TERN_ERR_SHAPE, TERN_ERR_VALUE (a type, layout or
+ * eps), TERN_ERR_ALIGN, before any launch; TERN_ERR_HIP.
+ */
+tern_status tern_rmsnorm(const void* x, tern_dtype x_type, int64_t x_stride, const void* residual,
+                         int64_t residual_stride, void* residual_out, int64_t residual_out_stride,
+                         tern_dtype residual_type, const void* weight, tern_dtype weight_type, float eps,
+                         int T, int k, int8_t* q, float* act_scale, tern_q_layout layout, void* y_bf16,
+                         int64_t y_stride, void* stream);
+
+/* Tokens of a cache page. */
+#define TERN_KV_PAGE 64
+
+/*
+ * Key/value cache in 8 bits: `pages` pages of 64 tokens, one fp32 scale per
+ * page and kv head for the keys and one for the values; value = code * scale.
+ * Device pointers, the caller's:
+ *   k [pages][heads][64][dim] int8: slot t of a page is its t-th token;
+ *   v [pages][heads][dim][64] int8: slot 16 i + 4 g + e at place 16 g + 4 i + e;
+ *   k_scale, v_scale [pages][heads].
+ * dim is 64, 128 or 256. Codes of slots that hold no token are unspecified.
+ */
+typedef struct {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t pages, heads, dim;
+} tern_kv_cache;
+
+/*
+ * The sequences of a call, ragged (device arrays, read when the kernels run):
+ *   q_begin [seqs + 1]: rows q_begin[s] .. q_begin[s+1]-1 of the call's token
+ *     matrices belong to sequence s, in order; they are its last tokens;
+ *   kv_len [seqs]: tokens of the sequence, this call's among them;
+ *   page_table [seqs][table_width]: page of its tokens 64 i .. 64 i + 63.
+ * max_q and max_kv bound the rows and tokens of a sequence (they size the
+ * launch); max_kv <= 64 table_width. The kernels check what they read: a
+ * sequence whose arrays contradict these bounds, and a page outside the
+ * cache, are left out (nothing is read or written for them; their attention
+ * rows are those of a sequence without those keys).
+ */
+typedef struct {
+  const int32_t* q_begin;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int32_t seqs, max_q, max_kv, table_width;
+} tern_kv_batch;
+
+/*
+ * Rotary positions with up to 255 axes: pair i (of `pairs`) turns elements i
+ * and pairs + i of a head by the angle whose (cosine, sine) stands in
+ * table[p][i][0..1] (fp32, [max_pos][pairs][2]), p = positions[axis[i]][token]
+ * clamped to [0, max_pos). axis: device uint8 [pairs], taken as axes - 1 where
+ * larger. pairs a multiple of 4, 2 pairs <= dim; elements from 2 pairs on do
+ * not turn.
+ */
+typedef struct {
+  const float* table;
+  const uint8_t* axis;
+  int32_t pairs, max_pos, axes;
+} tern_rope;
+
+/*
+ * Appends a call's tokens to the cache (device, async, one launch): q and k are
+ * turned by their positions (rope NULL: not), q is rounded to bf16 into q_out
+ * [tokens][q_heads][dim], k and v are quantised into the pages of their
+ * sequences. A page's scale becomes s = max(its scale, fl(max|new values| / 127))
+ * if it holds earlier tokens of the sequence, whose codes c become
+ * round-half-even(fl(fl(c s_old) / s)); else fl(max|new| / 127). New codes are
+ * clamp(round-half-even(fl(x / s)), -127, 127), zero where s is zero.
+ * A page that several sequences share must not be appended to (copy it first).
+ * k, v: [tokens] rows of heads * dim, k_stride and v_stride elements apart;
+ * q: rows of q_heads * dim, q_stride apart, or NULL (with q_out); all of
+ * `type`. positions: device int32 [axes][tokens] (with rope). Row starts and
+ * pointers 16-byte aligned (8 for bf16 inputs). Errors as tern_rmsnorm.
+ */
+tern_status tern_kv_append(const tern_kv_cache* cache, const tern_kv_batch* batch, int tokens,
+                           const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const void* q, int64_t q_stride, int q_heads, void* q_out_bf16,
+                           tern_dtype type, const tern_rope* rope, const int32_t* positions,
+                           void* stream);
+
+/*
+ * The stored values of every sequence's last q_begin[s+1] - q_begin[s] tokens
+ * (device, async): k_out and v_out [rows][heads][dim] bf16 (either NULL),
+ * code * scale rounded to nearest even. Rows of sequences that are left out
+ * (see tern_kv_batch) are not written.
+ */
+tern_status tern_kv_read(const tern_kv_cache* cache, const tern_kv_batch* batch, int rows,
+                         void* k_out_bf16, void* v_out_bf16, void* stream);
+
+/*
+ * Attention over the cache (device, async). Query row t of sequence s stands
+ * at position i = kv_len[s] - (q_begin[s+1] - t) and sees key j if j <= i and
+ * (window == 0 or j > i - window or j < sinks):
+ *   out[t][h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q[t][h] . k_j),
+ * over the keys it sees, kv head h / (q_heads / heads); a row that sees
+ * none is zero. q: bf16 [tokens] rows of q_heads * dim, q_stride elements
+ * apart; out: bf16 [tokens][q_heads][dim]. q_heads a multiple of
+ * cache->heads; scale > 0. The append of the call's tokens comes first.
+ * ws: device, tern_kv_attn_workspace_bytes() bytes for the same arguments
+ * (16-byte aligned; NULL if 0); calls that share it must not overlap.
+ * Scores and softmax statistics are fp32; probabilities enter the product with
+ * the values as fp16 (11 bits). v scales below 2^-100 count as 2^-100.
+ * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.
+ */
+tern_status tern_kv_attn(const tern_kv_cache* cache, const tern_kv_batch* batch, int tokens,
+                         const void* q_bf16, int64_t q_stride, int q_heads, float scale, int window,
+                         int sinks, void* out_bf16, void* ws, size_t ws_bytes, void* stream);
+/* (size_t)-1 if the arguments are invalid (tern_last_error says why). */
+size_t tern_kv_attn_workspace_bytes(const tern_kv_cache* cache, const tern_kv_batch* batch, int tokens,
+                                    int q_heads, int window, int sinks);
+
 /* Rung probe: number of kernel launches per rung since the last reset,
  * counted at the launch site of the kernel that actually ran. */
 void tern_probe_snapshot(uint64_t out[TERN_RUNG_COUNT]);
@@ -459,6 +594,11 @@ typedef enum {
   TERN_KERNEL_GEMV_T5,            /* gemv on base-3 (t5) weights: limbs of x on the i8 matrix cores */
   TERN_KERNEL_CHAIN,              /* tern_linear_chain: a chain of T = 1 projections in one launch */
   TERN_KERNEL_SMALLT_NARROW,      /* small_t / small_t_tiled on narrow layers: K split over workgroups, partials added in-launch */
+  TERN_KERNEL_RMSNORM,            /* tern_rmsnorm */
+  TERN_KERNEL_KV_APPEND,          /* tern_kv_append */
+  TERN_KERNEL_KV_READ,            /* tern_kv_read */
+  TERN_KERNEL_KV_ATTN,            /* tern_kv_attn: few rows per kv head, keys and values straight to registers */
+  TERN_KERNEL_KV_ATTN_JOIN,       /* tern_kv_attn: joins the runs of a split key axis */
   TERN_KERNEL_COUNT
 } tern_kernel;
 
@@ -466,8 +606,8 @@ typedef enum {
 void tern_kernel_probe_snapshot(uint64_t out[TERN_KERNEL_COUNT]);
 /* Bit i set: kernel i was launched by the most recent successful call on this
  * thread of tern_linear, tern_linear_s8_q, tern_debug_s8_acc,
- * tern_quant_act_s8, tern_quant_act_s8_rot or tern_stream_read (0 before
- * any). With TERN_DEBUG=1 the rung line of tern_linear names them too. */
+ * tern_quant_act_s8, tern_quant_act_s8_rot, tern_stream_read, tern_rmsnorm,
+ * tern_kv_append, tern_kv_read or tern_kv_attn (0 before any). With TERN_DEBUG=1 the rung line of tern_linear names them too. */
 uint64_t tern_last_kernels(void);
 /* Host-only dry run of the dispatcher (no HIP call): the kernel-id bit mask
  * (as tern_last_kernels) that tern_linear(T, N, K, G, rung) on weights of

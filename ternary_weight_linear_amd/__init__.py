@@ -14,6 +14,10 @@ Entry points mirror the C ABI in ``include/tern.h``:
 * ``linear``                   -- ``y = ternary_linear(x)`` with rung dispatch
 * ``linear_s8_q``              -- the s8 contraction on pre-quantised activations
 * ``debug_s8_acc``             -- the s8 rung's int32 group accumulators
+* ``rmsnorm`` / ``rmsnorm_s8`` -- RMS norm with the residual's addition, bf16 or 8-bit output
+* ``KVCache`` / ``KVBatch`` / ``Rope`` -- the 8-bit paged cache, a call's sequences, rotary positions
+* ``kv_append`` / ``kv_read``  -- new tokens into the cache (rotary q and k), stored values out of it
+* ``kv_attn`` / ``kv_attn_workspace`` -- attention over the cache (window and sinks optional)
 * ``probe_snapshot`` / ``probe_reset`` / ``last_rung`` / ``resolve_rung``
 * ``kernel_probe_snapshot`` / ``last_kernels`` -- which kernels ran
 
@@ -49,7 +53,7 @@ KERNELS = ("quant_s8", "quant_s8_row", "quant_s8_rot", "gemv_limb", "gemv_bf16",
            "smallt_resident", "smallt_limb_fused", "smallt_limb_prep", "smallt_limb_tile",
            "smallt_wave", "smallt_tile", "smallt_tile_reduce", "b16_prefill", "s8_mma",
            "s8_reduce", "s8_row", "s8_acc_export", "stream_read", "gemv_t5", "chain",
-           "smallt_narrow")
+           "smallt_narrow", "rmsnorm", "kv_append", "kv_read", "kv_attn", "kv_attn_join")
 
 # Symbols declared in include/tern.h (checked by the host tests).
 EXPORTS = ("tern_packed_code_bytes", "tern_scale_count", "tern_pack", "tern_unpack",
@@ -60,7 +64,8 @@ EXPORTS = ("tern_packed_code_bytes", "tern_scale_count", "tern_pack", "tern_unpa
            "tern_kernel_probe_snapshot", "tern_last_kernels", "tern_kernel_name",
            "tern_plan_kernels", "tern_linear_noalloc", "tern_packed_code_bytes_t5", "tern_pack_t5",
            "tern_unpack_t5", "tern_chain_table_bytes", "tern_chain_counter_bytes", "tern_chain_build",
-           "tern_linear_chain")
+           "tern_linear_chain", "tern_rmsnorm", "tern_kv_append", "tern_kv_read", "tern_kv_attn",
+           "tern_kv_attn_workspace_bytes")
 
 
 class TernError(RuntimeError):
@@ -85,6 +90,23 @@ class _ChainPlan(ctypes.Structure):
                 ("lds_bytes", ctypes.c_int32), ("waits", ctypes.c_int32)]
 
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("q_begin", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seqs", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("table_width", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("pairs", ctypes.c_int32),
+                ("max_pos", ctypes.c_int32), ("axes", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -98,6 +120,8 @@ def lib() -> ctypes.CDLL:
                           "`python -m ternary_weight_linear_amd.build` (hipcc, gfx950)")
     L = ctypes.CDLL(LIB_PATH)
     p, i, sz, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
+    l, f = ctypes.c_int64, ctypes.c_float
+    kc, kb = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
     sig = {
         "tern_packed_code_bytes": (sz, [i, i]),
         "tern_scale_count": (sz, [i, i, i]),
@@ -129,6 +153,11 @@ def lib() -> ctypes.CDLL:
         "tern_chain_counter_bytes": (sz, [i]),
         "tern_chain_build": (st, [ctypes.POINTER(_ChainItem), i, p, sz, ctypes.POINTER(_ChainPlan)]),
         "tern_linear_chain": (st, [ctypes.POINTER(_ChainPlan), p, p, sz, p, i, p]),
+        "tern_rmsnorm": (st, [p, i, l, p, l, p, l, i, p, i, f, i, i, p, p, i, p, l, p]),
+        "tern_kv_append": (st, [kc, kb, i, p, l, p, l, p, l, i, p, i, ctypes.POINTER(_Rope), p, p]),
+        "tern_kv_read": (st, [kc, kb, i, p, p, p]),
+        "tern_kv_attn": (st, [kc, kb, i, p, l, i, f, i, i, p, p, sz, p]),
+        "tern_kv_attn_workspace_bytes": (sz, [kc, kb, i, i, i, i]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -523,3 +552,288 @@ class Chain:
     def failed(self) -> bool:
         """True if a wait gave up (synchronises on the flag)."""
         return bool(self.error_flag.item())
+
+
+# ------------------------------------------------------ decoder operators
+
+KV_PAGE = 64
+
+
+def _type(t, name):
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return 0
+    if t.dtype == torch.bfloat16:
+        return 1
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _rows(t, name, shape, device):
+    """Checks a device matrix (or a matrix of heads) whose rows may lie apart:
+    HIP, float32 or bfloat16, its shape and device, each row contiguous.
+    Returns (type, row stride in elements)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    kind = _type(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    stride, want = t.stride(), 1
+    for d in range(t.dim() - 1, 0, -1):
+        if t.shape[d] != 1 and stride[d] != want:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        want *= t.shape[d]
+    return kind, stride[0] if t.shape[0] > 1 else max(want, stride[0])
+
+
+def _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream):
+    T, K = x.shape
+    xt, xs = _rows(x, "x", (T, K), x.device)
+    wt, _ = _rows(weight[None] if weight.dim() == 1 else weight, "weight", (1, K), x.device)
+    rp = op = None
+    rt = rs = os_ = 0
+    if residual is not None:
+        rt, rs = _rows(residual, "residual", (T, K), x.device)
+        if residual_out is None:
+            residual_out = residual
+        ot, os_ = _rows(residual_out, "residual_out", (T, K), x.device)
+        if ot != rt:
+            raise TypeError("residual_out must have the residual's type")
+        rp, op = residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    ys = 0
+    if y is not None:
+        yt, ys = _rows(y, "y", (T, K), x.device)
+        if yt != 1:
+            raise TypeError(f"y must be bfloat16, got {y.dtype}")
+    if q is not None:
+        _dev(q, _torch().int8, "q", (T, K), x.device)
+        _dev(scale, _torch().float32, "scale", (T,), x.device)
+    _check(lib().tern_rmsnorm(x.data_ptr(), xt, xs, rp, rs, op, os_, rt, weight.data_ptr(), wt, eps, T, K,
+                              None if q is None else q.data_ptr(), None if q is None else scale.data_ptr(),
+                              Q_LAYOUTS[layout], None if y is None else y.data_ptr(), ys, _stream(stream)))
+
+
+def rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, stream=None):
+    """y [T, K] bf16 = the RMS norm of h = x + residual times weight (device).
+    x and residual: float32 or bfloat16, rows may lie apart; h is written to
+    residual_out (default: the residual itself) in the residual's type."""
+    torch = _torch()
+    if y is None:
+        with _on(stream):
+            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    _norm(x, weight, eps, residual, residual_out, None, None, "row_major", y, stream)
+    return y
+
+
+def rmsnorm_s8(x, weight, eps=1e-6, residual=None, residual_out=None, q=None, scale=None, y=None,
+               layout="row_major", stream=None):
+    """rmsnorm with an 8-bit output: (q int8 [T, K] in `layout`, scale float32
+    [T]), as linear_s8_q takes them; `y` (bf16) is written too when given."""
+    torch = _torch()
+    with _on(stream):
+        if q is None:
+            q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream)
+    return q, scale
+
+
+class KVCache:
+    """An 8-bit paged key/value cache on the GPU: k int8 [pages, heads, 64, d],
+    v int8 [pages, heads, d, 64] (see tern_kv_cache in tern.h for the order of
+    its tokens), k_scale and v_scale float32 [pages, heads]."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        torch = _torch()
+        _dev(k, torch.int8, "k")
+        if k.dim() != 4 or k.shape[2] != KV_PAGE:
+            raise ValueError(f"k must be [pages, heads, {KV_PAGE}, d], got {tuple(k.shape)}")
+        pages, heads, _, d = k.shape
+        _dev(v, torch.int8, "v", (pages, heads, d, KV_PAGE), k.device)
+        _dev(k_scale, torch.float32, "k_scale", (pages, heads), k.device)
+        _dev(v_scale, torch.float32, "v_scale", (pages, heads), k.device)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.d, self.device = pages, heads, d, k.device
+        self._struct = _KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, d)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, d: int, device="cuda"):
+        torch = _torch()
+        return cls(torch.zeros((pages, heads, KV_PAGE, d), dtype=torch.int8, device=device),
+                   torch.zeros((pages, heads, d, KV_PAGE), dtype=torch.int8, device=device),
+                   torch.zeros((pages, heads), dtype=torch.float32, device=device),
+                   torch.zeros((pages, heads), dtype=torch.float32, device=device))
+
+
+class KVBatch:
+    """The sequences of a call: q_begin int32 [seqs + 1] (rows of the call's
+    token matrices), kv_len int32 [seqs] (tokens of each sequence, the call's
+    among them), page_table int32 [seqs, width]; max_q and max_kv bound the
+    rows and the tokens of a sequence. The arrays are read when the kernels
+    run, so a captured graph follows their updates."""
+
+    def __init__(self, q_begin, kv_len, page_table, max_q: int, max_kv: int):
+        torch = _torch()
+        _dev(page_table, torch.int32, "page_table")
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table must be [seqs, width], got {tuple(page_table.shape)}")
+        seqs, width = page_table.shape
+        _dev(kv_len, torch.int32, "kv_len", (seqs,), page_table.device)
+        _dev(q_begin, torch.int32, "q_begin", (seqs + 1,), page_table.device)
+        self.q_begin, self.kv_len, self.page_table = q_begin, kv_len, page_table
+        self.seqs, self.max_q, self.max_kv, self.device = seqs, int(max_q), int(max_kv), page_table.device
+        self._struct = _KvBatch(q_begin.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), seqs, self.max_q,
+                                self.max_kv, width)
+        self._ref = ctypes.byref(self._struct)
+
+
+class Rope:
+    """Rotary positions: table float32 [positions, pairs, 2] of (cosine, sine)
+    and axis uint8 [pairs], the row of a call's positions that turns each pair
+    (None: one axis). Pair i turns elements i and pairs + i of a head."""
+
+    def __init__(self, table, axis=None):
+        torch = _torch()
+        _dev(table, torch.float32, "table")
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError(f"table must be [positions, pairs, 2], got {tuple(table.shape)}")
+        if axis is None:
+            axis = torch.zeros((table.shape[1],), dtype=torch.uint8, device=table.device)
+        _dev(axis, torch.uint8, "axis", (table.shape[1],), table.device)
+        self.table, self.axis, self.device = table, axis, table.device
+
+    @classmethod
+    def make(cls, positions: int, pairs: int, base: float = 1e6, sections=None, interleaved: bool = False,
+             device="cuda"):
+        """The table of angles position * base^(-i / pairs), computed in 64 bits,
+        and the axis map of `sections` pairs per axis: axis after axis, or
+        (interleaved) the axes in turn while they have pairs left."""
+        torch = _torch()
+        if sections is not None and (sum(sections) != pairs or min(sections) < 0):
+            raise ValueError(f"sections {tuple(sections)} must add up to pairs={pairs}")
+        f = float(base) ** (-torch.arange(pairs, dtype=torch.float64) / pairs)
+        a = torch.arange(positions, dtype=torch.float64)[:, None] * f
+        table = torch.stack((a.cos(), a.sin()), -1).float().contiguous().to(device)
+        axis = None
+        if sections is not None:
+            order = [x for x, n in enumerate(sections) for _ in range(n)]
+            if interleaved:
+                order = [x for _, x in sorted((i, x) for x, n in enumerate(sections) for i in range(n))]
+            axis = torch.tensor(order, dtype=torch.uint8).to(device)
+        return cls(table, axis)
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Rope = None, positions=None,
+              stream=None):
+    """Appends k, v [tokens, heads, d] (float32 or bfloat16, rows may lie apart,
+    as in a fused projection's output) to the cache, k turned by its
+    positions; returns q [tokens, q_heads, d] turned and rounded to bf16 (None
+    without q). positions: int32 [axes, tokens] or [tokens]."""
+    torch = _torch()
+    tokens = k.shape[0]
+    kt, ks = _rows(k, "k", (tokens, cache.heads, cache.d), cache.device)
+    vt, vs = _rows(v, "v", (tokens, cache.heads, cache.d), cache.device)
+    qp = op = None
+    qs = heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        qt, qs = _rows(q, "q", (tokens, heads, cache.d), cache.device)
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty((tokens, heads, cache.d), dtype=torch.bfloat16, device=cache.device)
+        _dev(q_out, torch.bfloat16, "q_out", (tokens, heads, cache.d), cache.device)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+        if qt != kt:
+            raise TypeError("q, k and v must have one type")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if vt != kt:
+        raise TypeError("q, k and v must have one type")
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    r = pp = None
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        _dev(positions, torch.int32, "positions", (axes, tokens) if positions.dim() == 2 else (tokens,), cache.device)
+        if rope.device != cache.device:
+            raise ValueError(f"rope is on {rope.device}, the cache on {cache.device}")
+        r = ctypes.byref(_Rope(rope.table.data_ptr(), rope.axis.data_ptr(), rope.table.shape[1], rope.table.shape[0], axes))
+        pp = positions.data_ptr()
+    elif positions is not None:
+        raise ValueError("positions without rope")
+    _check(lib().tern_kv_append(cache._ref, batch._ref, tokens, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, heads, op,
+                                kt, r, pp, _stream(stream)))
+    return q_out
+
+
+def kv_read(cache: KVCache, batch: KVBatch, rows: int, k_out=None, v_out=None, stream=None):
+    """(k, v) bf16 [rows, heads, d]: the stored values of every sequence's last
+    q_begin[s + 1] - q_begin[s] tokens."""
+    torch = _torch()
+    shape = (rows, cache.heads, cache.d)
+    with _on(stream):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+    _dev(k_out, torch.bfloat16, "k_out", shape, cache.device)
+    _dev(v_out, torch.bfloat16, "v_out", shape, cache.device)
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    _check(lib().tern_kv_read(cache._ref, batch._ref, rows, k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
+    return k_out, v_out
+
+
+def kv_attn_workspace_bytes(cache: KVCache, batch: KVBatch, tokens: int, q_heads: int, window: int = 0,
+                            sinks: int = 0) -> int:
+    n = lib().tern_kv_attn_workspace_bytes(cache._ref, batch._ref, tokens, q_heads, window, sinks)
+    if n == ctypes.c_size_t(-1).value:
+        raise TernError(2, lib().tern_last_error().decode())
+    return n
+
+
+def kv_attn_workspace(cache: KVCache, batch: KVBatch, tokens: int, q_heads: int, window: int = 0, sinks: int = 0,
+                      stream=None):
+    """A workspace for kv_attn calls of these sizes (None if they need none),
+    for a caller that keeps one from call to call."""
+    n = kv_attn_workspace_bytes(cache, batch, tokens, q_heads, window, sinks)
+    if n == 0:
+        return None
+    with _on(stream):
+        return _torch().empty((n,), dtype=_torch().uint8, device=cache.device)
+
+
+def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, sinks: int = 0, out=None,
+            workspace=None, stream=None):
+    """out [tokens, q_heads, d] bf16: attention of q (bf16, rows may lie apart)
+    over the cache. A query at position i sees key j <= i, with a window only
+    those with j > i - window or j < sinks; a row that sees none is zero."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, d]")
+    tokens, heads, _ = q.shape
+    qt, qs = _rows(q, "q", (tokens, heads, cache.d), cache.device)
+    if qt != 1:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    if out is None:
+        with _on(stream):
+            out = torch.empty((tokens, heads, cache.d), dtype=torch.bfloat16, device=cache.device)
+    _dev(out, torch.bfloat16, "out", (tokens, heads, cache.d), cache.device)
+    if workspace is None:
+        workspace = kv_attn_workspace(cache, batch, tokens, heads, window, sinks, stream)
+    elif not workspace.is_cuda or workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(lib().tern_kv_attn(cache._ref, batch._ref, tokens, q.data_ptr(), qs, heads, scale, window, sinks,
+                              out.data_ptr(), wp, wb, _stream(stream)))
+    return out

@@ -63,6 +63,9 @@ UNITS = [
     ("tern_noalloc.hip", []),
     ("tern_chain.hip", []),
     ("tern_narrow.hip", []),
+    ("tern_norm.hip", []),
+    ("tern_cache.hip", []),
+    ("tern_attn.hip", []),
 ]
 
 

@@ -53,8 +53,9 @@ const char* const kKernelNames[TERN_KERNEL_COUNT] = {
     "smallt_resident", "smallt_limb_fused", "smallt_limb_prep", "smallt_limb_tile", "smallt_wave",
     "smallt_tile",     "smallt_tile_reduce", "b16_prefill",   "s8_mma",           "s8_reduce",
     "s8_row",          "s8_acc_export",     "stream_read",    "gemv_t5",          "chain",
-    "smallt_narrow"};
-static_assert(TERN_KERNEL_COUNT == 21, "one name per kernel id");
+    "smallt_narrow",   "rmsnorm",           "kv_append",      "kv_read",          "kv_attn",
+    "kv_attn_join"};
+static_assert(TERN_KERNEL_COUNT == 26, "one name per kernel id");
 
 // ------------------------------------------------------------ configuration
 
@@ -1473,6 +1474,8 @@ tern_status tern_debug_s8_acc(const int8_t* q, int T, const tern_weights* W, int
   if (err) return hip_fail(err, "s8 debug launch");
   return call_ok();
 }
+
+#include "tern_host_decoder.h"
 
 void tern_probe_snapshot(uint64_t out[TERN_RUNG_COUNT]) {
   for (int i = 0; i < TERN_RUNG_COUNT; ++i) out[i] = g_probe[i].load(std::memory_order_relaxed);

@@ -193,4 +193,86 @@ int copy_to_device(void* dst, const void* src, size_t bytes);  // synchronous; r
 constexpr size_t kNoallocScratchBytes = (size_t)TERN_NOALLOC_SCRATCH_BYTES;
 int noalloc_scratch(void** out);
 
+// ---- the decoder operators (tern_norm.hip, tern_cache.hip, tern_attn.hip).
+// Their launchers are weak references of the host layer: a build of
+// tern_host.cpp that links without these units (the sanitizer build of the
+// host tests) still loads, and a call that would launch one fails there.
+#define TERN_WEAK __attribute__((weak))
+
+struct NormArgs {
+  const void* x;
+  const void* r;  // residual in, or nullptr
+  void* r_out;
+  const void* w;
+  int8_t* q;         // or nullptr
+  float* act_scale;  // with q
+  uint16_t* y;       // bf16, or nullptr
+  int64_t x_stride, r_stride, r_out_stride, y_stride;  // elements
+  int x_type, r_type, w_type;  // tern_dtype; r_type -1: no residual
+  int T, K;
+  float eps;
+  bool operand_order;
+};
+constexpr int kNormMaxK = 32768;
+TERN_WEAK int launch_rmsnorm(const NormArgs& a, void* stream);
+
+constexpr int kKvPage = TERN_KV_PAGE;
+
+struct KvCache {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int heads, dim;
+};
+struct KvBatch {
+  const int32_t* q_begin;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int seqs, max_q, max_kv, table_width;
+};
+struct RopeArgs {
+  const float* table;
+  const uint8_t* axis;
+  const int32_t* positions;
+  int pairs, max_pos, axes;  // pairs 0: no rotation
+};
+struct KvAppendArgs {
+  KvCache cache;
+  KvBatch batch;
+  RopeArgs rope;
+  const void *k, *v, *q;  // q may be nullptr
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride;
+  int tokens, q_heads, type;
+};
+struct KvReadArgs {
+  KvCache cache;
+  KvBatch batch;
+  uint16_t *k_out, *v_out;  // either may be nullptr
+  int rows;
+};
+TERN_WEAK int64_t kv_append_blocks(const KvAppendArgs& a, int64_t* kv_blocks);
+TERN_WEAK int64_t kv_read_blocks(const KvReadArgs& a);
+TERN_WEAK int launch_kv_append(const KvAppendArgs& a, void* stream);
+TERN_WEAK int launch_kv_read(const KvReadArgs& a, void* stream);
+
+struct KvAttnArgs {
+  KvCache cache;
+  KvBatch batch;
+  const uint16_t* q;  // bf16 [tokens][q_heads][dim], rows q_stride apart
+  uint16_t* out;      // bf16 [tokens][q_heads][dim]
+  int64_t q_stride;
+  int tokens, q_heads, window, sinks;
+  float scale;
+};
+// Launch shape of the attention: row blocks of `rows` (token, head of the
+// group) rows per kv head, and the visible pages cut into `splits` runs of
+// `chunk` pages (joined by a second kernel when splits > 1).
+struct KvAttnPlan {
+  int rows, row_blocks, splits, chunk;
+};
+TERN_WEAK int launch_kv_attn(const KvAttnArgs& a, const KvAttnPlan& p, void* ws, void* stream);
+
 }  // namespace tern
