@@ -44,8 +44,9 @@ def _run(cmd):
         raise subprocess.CalledProcessError(r.returncode, cmd)
 
 
-# The s8 contraction reads every MFMA accumulator in its fp32 epilogue: keep
-# MFMA results in VGPRs (no accumulator-register round trips).
+# The s8 contraction reads every MFMA accumulator in its fp32 epilogue, the
+# attention rescales its own: keep MFMA results in VGPRs (no
+# accumulator-register round trips).
 S8_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
 
@@ -65,7 +66,7 @@ UNITS = [
     ("tern_narrow.hip", []),
     ("tern_norm.hip", []),
     ("tern_cache.hip", []),
-    ("tern_attn.hip", []),
+    ("tern_attn.hip", S8_FLAGS),
 ]
 
 

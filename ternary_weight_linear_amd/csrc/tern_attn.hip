@@ -37,6 +37,8 @@ namespace {
 using namespace dev;
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kNone = -__builtin_inff();
@@ -58,22 +60,29 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
   hi = __builtin_bit_cast(uint32_t, b);
 }
 __device__ __forceinline__ f16x8 codes8(uint32_t w0, uint32_t w1) {
-  u32x4 o;
   uint32_t a, b, c, d;
   codes_f16(w0, a, b);
   codes_f16(w1, c, d);
-  o = u32x4{a, b, c, d};
-  return __builtin_bit_cast(f16x8, o);
+  return __builtin_bit_cast(f16x8, u32x4{a, b, c, d});
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, f16x2));
 }
 
-// Maximum and sum over the four lanes that share lane & 15.
+// Maximum and sum over the four lanes that share lane & 15: the two halves
+// of the wave, then the two rows of 16 of each half, by register swaps.
 __device__ __forceinline__ float group_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float group_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // A sequence as the kernels see it; n = 0 if its arrays contradict the bounds.
@@ -110,7 +119,7 @@ __device__ __forceinline__ Pages pages_of(const KvAttnArgs& a, const Seq& s, int
 // Grid: (row block, kv head) x splits x seqs; 4 waves, wave w takes pages
 // w, w + 4, ... of the split's run.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnPlan plan, float* part) {
+__global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 3 : D * NT <= 256 ? 2 : 1) tern_kv_attn_kernel(KvAttnArgs a, KvAttnPlan plan, float* part) {
   constexpr int C = D / 64;   // 64-wide chunks of a head
   constexpr int HT = D / 16;  // 16-wide row tiles of O^T
   constexpr int R = 16 * NT;
@@ -134,16 +143,12 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
   f16x8 qf[NT][C][2];
   float qs[NT];
   int pos[NT];
-  int64_t at[NT];
-  bool valid[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = r0 + 16 * t + n;
-    valid[t] = r < rows;
     const int rr = min(r, rows - 1);
     const int tok = rr / group, h = head * group + rr % group;
     pos[t] = seq.kv - seq.n + tok;
-    at[t] = (int64_t)(seq.row0 + tok) * a.q_heads + h;
     const uint16_t* q = a.q + (int64_t)(seq.row0 + tok) * a.q_stride + (int64_t)h * D;
     u32x4 raw[C][2];
     uint32_t m = 0;
@@ -183,6 +188,11 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
     for (int i = 0; i < HT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
+  // Keys and values are asked for one buffer ahead of their use: a page's
+  // 16-byte loads (N of keys, N of values a lane) go through two buffers of B
+  // in turn, and each buffer is refilled as soon as it has been used.
+  constexpr int N = D / 16, B = N < 8 ? N : 8, H = N / B;
+  u32x4 buf[2][B];
   const int32_t* table = a.batch.page_table + (int64_t)sid * a.batch.table_width;
   for (int base = begin; base < end; base += 256) {
     // Page ids and scales of this wave's next 64 pages, one a lane.
@@ -199,17 +209,42 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
       }
     }
     vs = vs < kLeastScale ? kLeastScale : vs;
-    const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / vs;
+    const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / (vs * kPScale);
     const int steps = (min(end, base + 256) - base - wave + 3) >> 2;
+    // Part h (0..2H-1: keys, then values) of step i's page into its buffer. A
+    // page outside the cache reads page 0 instead, and is masked.
+    auto ask = [&](int i, int h) {
+      const int pid = max(__builtin_amdgcn_readlane(id, i), 0);
+      const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
+      if (h < H) {
+        const int8_t* p = a.cache.k + off + n * D + 16 * g;
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          const int x = h * B + j;  // tokens 16 (x / C) .., elements 64 (x % C) ..
+          buf[h & 1][j] = *(const u32x4*)(p + 16 * (x / C) * D + 64 * (x % C));
+        }
+      } else {
+        const int8_t* p = a.cache.v + off + n * kKvPage + 16 * g;
+#pragma unroll
+        for (int j = 0; j < B; ++j) buf[h & 1][j] = *(const u32x4*)(p + 16 * ((h - H) * B + j) * kKvPage);
+      }
+    };
+    if (steps > 0) {
+      ask(0, 0);
+      ask(0, 1);
+    }
     for (int i = 0; i < steps; ++i) {
-      const int pid = __builtin_amdgcn_readlane(id, i);
-      if (pid < 0) continue;  // a page outside the cache: no keys
+      // What follows part h in its buffer: part h + 2 of this page or the next one's.
+      auto refill = [&](int h) {
+        if (h + 2 < 2 * H)
+          ask(i, h + 2);
+        else if (i + 1 < steps)
+          ask(i + 1, h + 2 - 2 * H);
+      };
+      const bool absent = __builtin_amdgcn_readlane(id, i) < 0;
       const float ksc = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ks), i));
       const float lvs = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lv), i));
       const float ivs = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(iv), i));
-      const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
-      const int8_t* kp = a.cache.k + off + n * D + 16 * g;
-      const int8_t* vp = a.cache.v + off + n * kKvPage + 16 * g;
       const int j0 = pages.at(base + wave + 4 * i) * kKvPage;
 
       f32x4 s[NT][4];
@@ -218,10 +253,11 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
 #pragma unroll
         for (int b = 0; b < 4; ++b) s[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
+      for (int h = 0; h < H; ++h) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const u32x4 w = *(const u32x4*)(kp + 16 * b * D + 64 * c);
+        for (int j = 0; j < B; ++j) {
+          const int x = h * B + j, b = x / C, c = x % C;
+          const u32x4 w = buf[h & 1][j];
           const f16x8 k0 = codes8(w[0], w[1]), k1 = codes8(w[2], w[3]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -229,62 +265,82 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
             s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[t][c][1], s[t][b], 0, 0, 0);
           }
         }
+        refill(h);
+      }
 
       // Whether every row sees the whole page.
-      const bool whole = j0 + kKvPage - 1 <= pos_min &&
+      const bool whole = !absent && j0 + kKvPage - 1 <= pos_min &&
                          (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
       f16x8 pf[NT][2];
+      float alpha[NT];
+      auto softmax = [&](auto masked) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float f = ksc * qs[t];
-        f = f > kMostFactor ? kMostFactor : f;  // NaN stays
-        uint32_t see = 0xffffu;
-        if (!whole) {
-          see = 0;
+        for (int t = 0; t < NT; ++t) {
+          float f = ksc * qs[t];
+          f = f > kMostFactor ? kMostFactor : f;  // NaN stays
+          float mx = kNone;
+          bool see[4][4];
 #pragma unroll
           for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = j0 + 16 * b + 4 * g + e;
-              const bool v = j <= pos[t] && (!a.window || j > pos[t] - a.window || j < a.sinks);
-              see |= (v ? 1u : 0u) << (4 * b + e);
+              if constexpr (decltype(masked)::value) {
+                const int j = j0 + 16 * b + 4 * g + e;
+                see[b][e] = !absent && j <= pos[t] && (!a.window || j > pos[t] - a.window || j < a.sinks);
+                mx = fmaxf(mx, see[b][e] ? s[t][b][e] : kNone);
+              } else {
+                mx = fmaxf(mx, s[t][b][e]);
+              }
             }
-        }
-        float mx = kNone;
+          mx = group_max(mx);
+          const float top = mx == kNone ? kNone : __builtin_fmaf(mx, f, lvs);
+          const float Mn = fmaxf(M[t], top);
+          const float base2 = Mn == kNone ? 0.f : Mn;
+          alpha[t] = __builtin_amdgcn_exp2f(M[t] - base2);
+          M[t] = Mn;
+          const float add = (lvs - base2) + 15.f;  // p' in fp16 stands times 2^15
+          float sum = 0.f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+          for (int b = 0; b < 4; ++b) {
+            float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, see >> (4 * b + e) & 1 ? s[t][b][e] : kNone);
-        mx = group_max(mx);
-        const float top = mx == kNone ? kNone : __builtin_fmaf(mx, f, lvs);
-        const float Mn = fmaxf(M[t], top);
-        const float base2 = Mn == kNone ? 0.f : Mn;
-        const float alpha = __builtin_amdgcn_exp2f(M[t] - base2);
-        M[t] = Mn;
-        const float add = lvs - base2;
-        float sum = 0.f;
+            for (int e = 0; e < 4; ++e) {
+              p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][e], f, add));
+              if constexpr (decltype(masked)::value) p[e] = see[b][e] ? p[e] : 0.f;
+              sum += p[e];
+            }
+            const u32x2 w = {pack_f16(p[0], p[1]), pack_f16(p[2], p[3])};
+            const f16x4 v = __builtin_bit_cast(f16x4, w);
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][e], f, add));
-            p = see >> (4 * b + e) & 1 ? p : 0.f;
-            sum += p;
-            pf[t][b >> 1][4 * (b & 1) + e] = (_Float16)(p * kPScale);
+            for (int e = 0; e < 4; ++e) pf[t][b >> 1][4 * (b & 1) + e] = v[e];
           }
-        L[t] = __builtin_fmaf(L[t], alpha, sum * ivs);
-#pragma unroll
-        for (int h = 0; h < HT; ++h) o[t][h] *= alpha;
-      }
-#pragma unroll
-      for (int h = 0; h < HT; ++h) {
-        const u32x4 w = *(const u32x4*)(vp + 16 * h * kKvPage);
-        const f16x8 v0 = codes8(w[0], w[1]), v1 = codes8(w[2], w[3]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          o[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][h], 0, 0, 0);
-          o[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][h], 0, 0, 0);
+          L[t] = __builtin_fmaf(L[t], alpha[t], sum * ivs);
         }
+      };
+      if (whole)
+        softmax(std::false_type{});
+      else
+        softmax(std::true_type{});
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (__any(alpha[t] != 1.f)) {  // a maximum moved (or a row is NaN)
+#pragma unroll
+          for (int x = 0; x < HT; ++x) o[t][x] *= alpha[t];
+        }
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          const int x = h * B + j;
+          const u32x4 w = buf[(H + h) & 1][j];
+          const f16x8 v0 = codes8(w[0], w[1]), v1 = codes8(w[2], w[3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][x], 0, 0, 0);
+            o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][x], 0, 0, 0);
+          }
+        }
+        refill(H + h);
       }
     }
   }
@@ -323,12 +379,18 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
     __syncthreads();
   }
   if (wave != 0) return;
+  // Row of the lane in [tokens][q_heads], or -1 past the sequence's last.
+  auto row_at = [&](int t) -> int64_t {
+    const int r = r0 + 16 * t + n;
+    return r < rows ? (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group : -1;
+  };
   if (splits <= 1) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      if (!valid[t]) continue;
+      const int64_t at = row_at(t);
+      if (at < 0) continue;
       const float inv = L[t] == 0.f ? 0.f : 1.0f / (L[t] * kPScale);
-      uint16_t* out = a.out + at[t] * D + 4 * g;
+      uint16_t* out = a.out + at * D + 4 * g;
 #pragma unroll
       for (int h = 0; h < HT; ++h)
         *(uint2*)(out + 16 * h) =
@@ -341,16 +403,23 @@ __global__ void __launch_bounds__(256) tern_kv_attn_kernel(KvAttnArgs a, KvAttnP
   float* pm = part + (int64_t)plan.splits * all * D + (int64_t)split * all * 2;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if (!valid[t]) continue;
+    const int64_t at = row_at(t);
+    if (at < 0) continue;
 #pragma unroll
-    for (int h = 0; h < HT; ++h) *(f32x4*)(po + at[t] * D + 16 * h + 4 * g) = o[t][h];
-    if (g == 0) *(float2*)(pm + at[t] * 2) = float2{M[t], L[t]};
+    for (int h = 0; h < HT; ++h) *(f32x4*)(po + at * D + 16 * h + 4 * g) = o[t][h];
+    if (g == 0) *(float2*)(pm + at * 2) = float2{M[t], L[t]};
   }
 }
 
-// Joins the runs of each row; one workgroup of D threads a row.
+// Joins the runs of each row; one workgroup of 256 threads a row. Every
+// D/4 threads add the runs s, s + G, ... of four elements each, and the G
+// partial sums are added in order, so a row's result does not depend on timing.
 template <int D>
-__global__ void __launch_bounds__(D) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* part) {
+__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* part) {
+  constexpr int G = 1024 / D;
+  __shared__ float weight[kKvMaxSplits];
+  __shared__ float red[8];
+  __shared__ f32x4 sums[256];
   const int heads = a.cache.heads, group = a.q_heads / heads;
   const Seq seq = sequence(a, blockIdx.z);
   const int tok = blockIdx.x, h = blockIdx.y;
@@ -362,19 +431,47 @@ __global__ void __launch_bounds__(D) tern_kv_attn_join_kernel(KvAttnArgs a, KvAt
   if (splits <= 1) return;  // written by its workgroup
   const int64_t all = (int64_t)a.tokens * a.q_heads;
   const int64_t at = (int64_t)(seq.row0 + tok) * a.q_heads + h;
-  const float* pm = part + (int64_t)plan.splits * all * D + at * 2;
+  const float2* pm = (const float2*)(part + (int64_t)plan.splits * all * D) + at;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float M = kNone;
-  for (int s = 0; s < splits; ++s) M = fmaxf(M, pm[s * all * 2]);
-  const float b = M == kNone ? 0.f : M;
-  float L = 0.f, o = 0.f;
-  for (int s = 0; s < splits; ++s) {
-    const float2 ml = *(const float2*)(pm + s * all * 2);
-    const float w = __builtin_amdgcn_exp2f(ml.x - b);
-    L = __builtin_fmaf(ml.y, w, L);
-    o = __builtin_fmaf(part[(s * all + at) * D + threadIdx.x], w, o);
+  float2 ml[kKvMaxSplits / 256];
+#pragma unroll
+  for (int u = 0; u < kKvMaxSplits / 256; ++u) {
+    const int s = threadIdx.x + 256 * u;
+    ml[u] = s < splits ? pm[s * all] : float2{kNone, 0.f};
+    M = fmaxf(M, ml[u].x);
   }
-  const float v = L == 0.f ? 0.f : o / (L * kPScale);
-  a.out[at * D + threadIdx.x] = (uint16_t)pack_bf16(v, 0.f);
+  for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
+  if (lane == 0) red[wave] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float b = M == kNone ? 0.f : M;
+  float L = 0.f;
+#pragma unroll
+  for (int u = 0; u < kKvMaxSplits / 256; ++u) {
+    const int s = threadIdx.x + 256 * u;
+    const float w = __builtin_amdgcn_exp2f(ml[u].x - b);
+    if (s < splits) {
+      weight[s] = w;
+      L = __builtin_fmaf(ml[u].y, w, L);
+    }
+  }
+  L = wave_sum(L);
+  if (lane == 0) red[4 + wave] = L;
+  __syncthreads();
+  L = (red[4] + red[5]) + (red[6] + red[7]);
+  const int e = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
+  const f32x4* po = (const f32x4*)(part + at * D) + e;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = grp; s < splits; s += G) o += po[s * all * (D / 4)] * weight[s];
+  sums[threadIdx.x] = o;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int x = 1; x < G; ++x) o += sums[e + x * (D / 4)];
+  const float inv = L == 0.f ? 0.f : 1.0f / (L * kPScale);
+  *(uint2*)(a.out + at * D + 4 * e) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 template <int D, int NT>
@@ -394,7 +491,7 @@ int launch(const KvAttnArgs& a, const KvAttnPlan& p, float* part, hipStream_t st
   const hipError_t e = p.rows == 16 ? go<D, 1>(a, p, part, st) : go<D, 2>(a, p, part, st);
   if (kernel_launched((int)e, TERN_KERNEL_KV_ATTN)) return (int)e;
   if (p.splits == 1) return 0;
-  tern_kv_attn_join_kernel<D><<<dim3(a.batch.max_q, a.q_heads, a.batch.seqs), dim3(D), 0, st>>>(a, p, part);
+  tern_kv_attn_join_kernel<D><<<dim3(a.batch.max_q, a.q_heads, a.batch.seqs), dim3(256), 0, st>>>(a, p, part);
   return kernel_launched((int)hipGetLastError(), TERN_KERNEL_KV_ATTN_JOIN);
 }
 

@@ -209,7 +209,7 @@ tern_status tern_kv_attn(const tern_kv_cache* cache, const tern_kv_batch* batch,
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_ERR_WORKSPACE, "tern_kv_attn needs %zu bytes of workspace, got %zu", need, ws ? ws_bytes : (size_t)0);
   if (need && !aligned16(ws)) return fail(TERN_ERR_ALIGN, "the workspace must be 16-byte aligned");
-  if ((int64_t)p.row_blocks * a.cache.heads > kMaxGrid || p.splits > 65535)
+  if ((int64_t)p.row_blocks * a.cache.heads > kMaxGrid || p.splits > tern::kKvMaxSplits)
     return fail(TERN_ERR_SHAPE, "tern_kv_attn: too many rows or pages for one launch");
   if (!tern::launch_kv_attn) return no_unit();
   a.q = (const uint16_t*)q_bf16, a.out = (uint16_t*)out_bf16, a.q_stride = q_stride, a.scale = scale;

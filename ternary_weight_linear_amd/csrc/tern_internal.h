@@ -273,6 +273,7 @@ struct KvAttnArgs {
 struct KvAttnPlan {
   int rows, row_blocks, splits, chunk;
 };
+constexpr int kKvMaxSplits = 1024;
 TERN_WEAK int launch_kv_attn(const KvAttnArgs& a, const KvAttnPlan& p, void* ws, void* stream);
 
 }  // namespace tern
