@@ -280,10 +280,20 @@ def _torch():
     return torch
 
 
+def _current_stream() -> int:
+    """Handle of the current device's current stream. PyTorch's own lookup of
+    it, without the Stream object that torch.cuda.current_stream() builds
+    around it (3 us a call, as long as a launch)."""
+    c = _torch()._C
+    try:
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    except (AttributeError, RuntimeError):  # another PyTorch, or CUDA not initialised yet
+        return _torch().cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
-    torch = _torch()
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return ctypes.c_void_p(_current_stream())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -559,73 +569,92 @@ class Chain:
 KV_PAGE = 64
 
 
-def _type(t, name):
-    torch = _torch()
-    if t.dtype == torch.float32:
-        return 0
-    if t.dtype == torch.bfloat16:
-        return 1
-    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+_KINDS = {}  # dtype -> tern_dtype
 
 
 def _rows(t, name, shape, device):
     """Checks a device matrix (or a matrix of heads) whose rows may lie apart:
-    HIP, float32 or bfloat16, its shape and device, each row contiguous.
-    Returns (type, row stride in elements)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    kind = _type(t, name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    float32 or bfloat16, its shape and device, each row contiguous. Returns
+    (type, row stride in elements)."""
+    try:
+        kind, size, where, whole = _KINDS.get(t.dtype), t.shape, t.device, t.is_contiguous()
+    except AttributeError:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor") from None
+    if kind is None:
+        torch = _torch()
+        _KINDS.update({torch.float32: 0, torch.bfloat16: 1})
+        kind = _KINDS.get(t.dtype)
+        if kind is None:
+            raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
+    if where != device:
+        raise ValueError(f"{name} is on {where}, expected {device}")
+    row = 1
+    for n in size[1:]:
+        row *= n
+    if whole:
+        return kind, row
     stride, want = t.stride(), 1
-    for d in range(t.dim() - 1, 0, -1):
-        if t.shape[d] != 1 and stride[d] != want:
+    for d in range(len(size) - 1, 0, -1):
+        if size[d] != 1 and stride[d] != want:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        want *= t.shape[d]
-    return kind, stride[0] if t.shape[0] > 1 else max(want, stride[0])
+        want *= size[d]
+    return kind, stride[0] if size[0] > 1 else max(row, stride[0])
 
 
-def _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream):
+def _on_gpu(t, name):
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    return t.device
+
+
+def _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream, made=False):
+    """`made`: q, scale and y are this module's own, of the right shape."""
+    device = _on_gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
     T, K = x.shape
-    xt, xs = _rows(x, "x", (T, K), x.device)
-    wt, _ = _rows(weight[None] if weight.dim() == 1 else weight, "weight", (1, K), x.device)
-    rp = op = None
-    rt = rs = os_ = 0
+    xt, xs = _rows(x, "x", (T, K), device)
+    wt, _ = _rows(weight if weight.dim() == 2 else weight[None], "weight", (1, K), device)
+    rp = op = qp = sp = yp = None
+    rt = rs = os_ = ys = 0
     if residual is not None:
-        rt, rs = _rows(residual, "residual", (T, K), x.device)
-        if residual_out is None:
-            residual_out = residual
-        ot, os_ = _rows(residual_out, "residual_out", (T, K), x.device)
-        if ot != rt:
-            raise TypeError("residual_out must have the residual's type")
-        rp, op = residual.data_ptr(), residual_out.data_ptr()
+        rt, rs = _rows(residual, "residual", (T, K), device)
+        rp = residual.data_ptr()
+        if residual_out is None or residual_out is residual:
+            op, os_ = rp, rs
+        else:
+            ot, os_ = _rows(residual_out, "residual_out", (T, K), device)
+            if ot != rt:
+                raise TypeError("residual_out must have the residual's type")
+            op = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
-    ys = 0
     if y is not None:
-        yt, ys = _rows(y, "y", (T, K), x.device)
+        yt, ys = (1, K) if made else _rows(y, "y", (T, K), device)
         if yt != 1:
             raise TypeError(f"y must be bfloat16, got {y.dtype}")
+        yp = y.data_ptr()
     if q is not None:
-        _dev(q, _torch().int8, "q", (T, K), x.device)
-        _dev(scale, _torch().float32, "scale", (T,), x.device)
-    _check(lib().tern_rmsnorm(x.data_ptr(), xt, xs, rp, rs, op, os_, rt, weight.data_ptr(), wt, eps, T, K,
-                              None if q is None else q.data_ptr(), None if q is None else scale.data_ptr(),
-                              Q_LAYOUTS[layout], None if y is None else y.data_ptr(), ys, _stream(stream)))
+        if not made:
+            _dev(q, _torch().int8, "q", (T, K), device)
+            _dev(scale, _torch().float32, "scale", (T,), device)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    _check(lib().tern_rmsnorm(x.data_ptr(), xt, xs, rp, rs, op, os_, rt, weight.data_ptr(), wt, eps, T, K, qp, sp,
+                              Q_LAYOUTS[layout], yp, ys, _stream(stream)))
 
 
 def rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, stream=None):
     """y [T, K] bf16 = the RMS norm of h = x + residual times weight (device).
     x and residual: float32 or bfloat16, rows may lie apart; h is written to
     residual_out (default: the residual itself) in the residual's type."""
-    torch = _torch()
-    if y is None:
+    made = y is None
+    if made:
+        torch = _torch()
         with _on(stream):
             y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    _norm(x, weight, eps, residual, residual_out, None, None, "row_major", y, stream)
+    _norm(x, weight, eps, residual, residual_out, None, None, "row_major", y, stream, made)
     return y
 
 
@@ -633,13 +662,15 @@ def rmsnorm_s8(x, weight, eps=1e-6, residual=None, residual_out=None, q=None, sc
                layout="row_major", stream=None):
     """rmsnorm with an 8-bit output: (q int8 [T, K] in `layout`, scale float32
     [T]), as linear_s8_q takes them; `y` (bf16) is written too when given."""
-    torch = _torch()
-    with _on(stream):
-        if q is None:
-            q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        if scale is None:
-            scale = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
-    _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream)
+    made = q is None and scale is None and y is None
+    if q is None or scale is None:
+        torch = _torch()
+        with _on(stream):
+            if q is None:
+                q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+            if scale is None:
+                scale = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream, made)
     return q, scale
 
 
@@ -707,6 +738,15 @@ class Rope:
             axis = torch.zeros((table.shape[1],), dtype=torch.uint8, device=table.device)
         _dev(axis, torch.uint8, "axis", (table.shape[1],), table.device)
         self.table, self.axis, self.device = table, axis, table.device
+        self._refs = {}
+
+    def _ref(self, axes: int):
+        """The C struct for positions of so many axes (made once for each)."""
+        r = self._refs.get(axes)
+        if r is None:
+            r = self._refs[axes] = ctypes.byref(_Rope(self.table.data_ptr(), self.axis.data_ptr(), self.table.shape[1],
+                                                      self.table.shape[0], axes))
+        return r
 
     @classmethod
     def make(cls, positions: int, pairs: int, base: float = 1e6, sections=None, interleaved: bool = False,
@@ -729,44 +769,49 @@ class Rope:
         return cls(table, axis)
 
 
+def _same_device(batch, cache):
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+
+
 def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Rope = None, positions=None,
               stream=None):
     """Appends k, v [tokens, heads, d] (float32 or bfloat16, rows may lie apart,
     as in a fused projection's output) to the cache, k turned by its
     positions; returns q [tokens, q_heads, d] turned and rounded to bf16 (None
     without q). positions: int32 [axes, tokens] or [tokens]."""
-    torch = _torch()
+    device, d = cache.device, cache.d
     tokens = k.shape[0]
-    kt, ks = _rows(k, "k", (tokens, cache.heads, cache.d), cache.device)
-    vt, vs = _rows(v, "v", (tokens, cache.heads, cache.d), cache.device)
-    qp = op = None
-    qs = heads = 0
+    shape = (tokens, cache.heads, d)
+    kt, ks = _rows(k, "k", shape, device)
+    vt, vs = _rows(v, "v", shape, device)
+    qt, qp, op, qs, heads = kt, None, None, 0, 0
     if q is not None:
         heads = q.shape[1]
-        qt, qs = _rows(q, "q", (tokens, heads, cache.d), cache.device)
+        shape = (tokens, heads, d)
+        qt, qs = _rows(q, "q", shape, device)
         if q_out is None:
+            torch = _torch()
             with _on(stream):
-                q_out = torch.empty((tokens, heads, cache.d), dtype=torch.bfloat16, device=cache.device)
-        _dev(q_out, torch.bfloat16, "q_out", (tokens, heads, cache.d), cache.device)
+                q_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        else:
+            _dev(q_out, _torch().bfloat16, "q_out", shape, device)
         qp, op = q.data_ptr(), q_out.data_ptr()
-        if qt != kt:
-            raise TypeError("q, k and v must have one type")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if vt != kt:
+    if not kt == vt == qt:
         raise TypeError("q, k and v must have one type")
-    if batch.device != cache.device:
-        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    _same_device(batch, cache)
     r = pp = None
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-        _dev(positions, torch.int32, "positions", (axes, tokens) if positions.dim() == 2 else (tokens,), cache.device)
-        if rope.device != cache.device:
-            raise ValueError(f"rope is on {rope.device}, the cache on {cache.device}")
-        r = ctypes.byref(_Rope(rope.table.data_ptr(), rope.axis.data_ptr(), rope.table.shape[1], rope.table.shape[0], axes))
-        pp = positions.data_ptr()
+        one = positions.dim() == 1
+        axes = 1 if one else positions.shape[0]
+        _dev(positions, _torch().int32, "positions", (tokens,) if one else (axes, tokens), device)
+        if rope.device != device:
+            raise ValueError(f"rope is on {rope.device}, the cache on {device}")
+        r, pp = rope._ref(axes), positions.data_ptr()
     elif positions is not None:
         raise ValueError("positions without rope")
     _check(lib().tern_kv_append(cache._ref, batch._ref, tokens, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, heads, op,
@@ -777,17 +822,18 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Ro
 def kv_read(cache: KVCache, batch: KVBatch, rows: int, k_out=None, v_out=None, stream=None):
     """(k, v) bf16 [rows, heads, d]: the stored values of every sequence's last
     q_begin[s + 1] - q_begin[s] tokens."""
-    torch = _torch()
+    bf16 = _torch().bfloat16
     shape = (rows, cache.heads, cache.d)
     with _on(stream):
         if k_out is None:
-            k_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+            k_out = _torch().empty(shape, dtype=bf16, device=cache.device)
+        else:
+            _dev(k_out, bf16, "k_out", shape, cache.device)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    _dev(k_out, torch.bfloat16, "k_out", shape, cache.device)
-    _dev(v_out, torch.bfloat16, "v_out", shape, cache.device)
-    if batch.device != cache.device:
-        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+            v_out = _torch().empty(shape, dtype=bf16, device=cache.device)
+        else:
+            _dev(v_out, bf16, "v_out", shape, cache.device)
+    _same_device(batch, cache)
     _check(lib().tern_kv_read(cache._ref, batch._ref, rows, k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
     return k_out, v_out
 
@@ -816,22 +862,23 @@ def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, si
     """out [tokens, q_heads, d] bf16: attention of q (bf16, rows may lie apart)
     over the cache. A query at position i sees key j <= i, with a window only
     those with j > i - window or j < sinks; a row that sees none is zero."""
-    torch = _torch()
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    device = cache.device
+    if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, d]")
-    tokens, heads, _ = q.shape
-    qt, qs = _rows(q, "q", (tokens, heads, cache.d), cache.device)
+    tokens, heads = q.shape[:2]
+    shape = (tokens, heads, cache.d)
+    qt, qs = _rows(q, "q", shape, device)
     if qt != 1:
         raise TypeError(f"q must be bfloat16, got {q.dtype}")
-    if batch.device != cache.device:
-        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    _same_device(batch, cache)
     if out is None:
         with _on(stream):
-            out = torch.empty((tokens, heads, cache.d), dtype=torch.bfloat16, device=cache.device)
-    _dev(out, torch.bfloat16, "out", (tokens, heads, cache.d), cache.device)
+            out = _torch().empty(shape, dtype=q.dtype, device=device)
+    else:
+        _dev(out, q.dtype, "out", shape, device)
     if workspace is None:
         workspace = kv_attn_workspace(cache, batch, tokens, heads, window, sinks, stream)
-    elif not workspace.is_cuda or workspace.device != cache.device or not workspace.is_contiguous():
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib().tern_kv_attn(cache._ref, batch._ref, tokens, q.data_ptr(), qs, heads, scale, window, sinks,

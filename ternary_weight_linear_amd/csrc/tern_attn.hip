@@ -139,29 +139,91 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
   if (begin >= end && split > 0) return;
   const int splits = (pages.count + plan.chunk - 1) / plan.chunk;  // of this row block
 
-  // The lane's query rows: position, element offset, fp16 operands.
-  f16x8 qf[NT][C][2];
-  float qs[NT];
+  // Page ids and scales of this wave's next 64 pages, one a lane; then keys
+  // and values, asked for one buffer ahead of their use: a page's 16-byte
+  // loads (N of keys, N of values a lane) go through two buffers of B in turn,
+  // and each buffer is refilled as soon as it has been used. Streamed once:
+  // non-temporal.
+  constexpr int N = D / 16, B = N < 8 ? N : 8, H = N / B;
+  u32x4 buf[2][B];
+  const int32_t* table = a.batch.page_table + (int64_t)sid * a.batch.table_width;
+  int id = -1, steps = 0;
+  float ks = 0.f, vs = 0.f;
+  auto ids = [&](int base) {
+    const int mine = base + wave + 4 * lane;
+    steps = (min(end, base + 256) - base - wave + 3) >> 2;
+    id = mine < end ? table[pages.at(mine)] : -1;
+  };
+  auto scales = [&]() {
+    if (id >= a.cache.pages) id = -1;
+    ks = vs = 0.f;
+    if (id >= 0) {
+      const int64_t ph = (int64_t)id * heads + head;
+      ks = a.cache.k_scale[ph];
+      vs = a.cache.v_scale[ph];
+    }
+  };
+  // Part h (0..2H-1: keys, then values) of step i's page into its buffer. A
+  // page outside the cache reads page 0 instead, and is masked.
+  auto ask = [&](int i, int h) {
+    const int pid = max(__builtin_amdgcn_readlane(id, i), 0);
+    const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
+    if (h < H) {
+      const int8_t* p = a.cache.k + off + n * D + 16 * g;
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const int x = h * B + j;  // tokens 16 (x / C) .., elements 64 (x % C) ..
+        buf[h & 1][j] = __builtin_nontemporal_load((const u32x4*)(p + 16 * (x / C) * D + 64 * (x % C)));
+      }
+    } else {
+      const int8_t* p = a.cache.v + off + n * kKvPage + 16 * g;
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        buf[h & 1][j] = __builtin_nontemporal_load((const u32x4*)(p + 16 * ((h - H) * B + j) * kKvPage));
+    }
+  };
+  auto start = [&]() {
+    scales();
+    if (steps > 0) {
+      ask(0, 0);
+      ask(0, 1);
+    }
+  };
+  // The chain of dependent loads at the start (lengths, page ids, scales and
+  // codes) is what a short call waits for: everything is asked for as soon as
+  // its address is known, the query rows between the ids and the codes.
+  ids(begin);
+  u32x4 raw[NT][C][2];
   int pos[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = r0 + 16 * t + n;
-    const int rr = min(r, rows - 1);
+    const int rr = min(r0 + 16 * t + n, rows - 1);
     const int tok = rr / group, h = head * group + rr % group;
     pos[t] = seq.kv - seq.n + tok;
     const uint16_t* q = a.q + (int64_t)(seq.row0 + tok) * a.q_stride + (int64_t)h * D;
-    u32x4 raw[C][2];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) raw[t][c][k] = *(const u32x4*)(q + 64 * c + 16 * g + 8 * k);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  start();
+  __builtin_amdgcn_sched_barrier(0);
+
+  // The query rows as fp16 operands, each brought to [1, 2) by a power of two.
+  f16x8 qf[NT][C][2];
+  float qs[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
     uint32_t m = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        raw[c][k] = *(const u32x4*)(q + 64 * c + 16 * g + 8 * k);
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, max((raw[c][k][i] << 16) & 0x7fff0000u, raw[c][k][i] & 0x7fff0000u));
-      }
-    m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        for (int i = 0; i < 4; ++i)
+          m = max(m, max((raw[t][c][k][i] << 16) & 0x7fff0000u, raw[t][c][k][i] & 0x7fff0000u));
+    m = __float_as_uint(group_max(__uint_as_float(min(m, 0x7f800000u))));  // a NaN takes infinity's exponent
     // 2^e <= max|q| < 2^(e+1); rows of zeros and of subnormals take e = -126
     const int e = min(max((int)(m >> 23) - 127, -126), 126);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -172,8 +234,8 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          qf[t][c][k][2 * i] = (_Float16)(bf16_lo(raw[c][k][i]) * down);
-          qf[t][c][k][2 * i + 1] = (_Float16)(bf16_hi(raw[c][k][i]) * down);
+          qf[t][c][k][2 * i] = (_Float16)(bf16_lo(raw[t][c][k][i]) * down);
+          qf[t][c][k][2 * i + 1] = (_Float16)(bf16_hi(raw[t][c][k][i]) * down);
         }
   }
   const int pos_min = seq.kv - seq.n + r0 / group, pos_max = seq.kv - seq.n + rlast / group;
@@ -188,51 +250,9 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
     for (int i = 0; i < HT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // Keys and values are asked for one buffer ahead of their use: a page's
-  // 16-byte loads (N of keys, N of values a lane) go through two buffers of B
-  // in turn, and each buffer is refilled as soon as it has been used.
-  constexpr int N = D / 16, B = N < 8 ? N : 8, H = N / B;
-  u32x4 buf[2][B];
-  const int32_t* table = a.batch.page_table + (int64_t)sid * a.batch.table_width;
-  for (int base = begin; base < end; base += 256) {
-    // Page ids and scales of this wave's next 64 pages, one a lane.
-    const int mine = base + wave + 4 * lane;
-    int id = -1;
-    float ks = 0.f, vs = 0.f;
-    if (mine < end) {
-      id = table[pages.at(mine)];
-      if (id >= a.cache.pages) id = -1;
-      if (id >= 0) {
-        const int64_t ph = (int64_t)id * heads + head;
-        ks = a.cache.k_scale[ph];
-        vs = a.cache.v_scale[ph];
-      }
-    }
+  for (int base = begin; base < end;) {
     vs = vs < kLeastScale ? kLeastScale : vs;
     const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / (vs * kPScale);
-    const int steps = (min(end, base + 256) - base - wave + 3) >> 2;
-    // Part h (0..2H-1: keys, then values) of step i's page into its buffer. A
-    // page outside the cache reads page 0 instead, and is masked.
-    auto ask = [&](int i, int h) {
-      const int pid = max(__builtin_amdgcn_readlane(id, i), 0);
-      const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
-      if (h < H) {
-        const int8_t* p = a.cache.k + off + n * D + 16 * g;
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          const int x = h * B + j;  // tokens 16 (x / C) .., elements 64 (x % C) ..
-          buf[h & 1][j] = *(const u32x4*)(p + 16 * (x / C) * D + 64 * (x % C));
-        }
-      } else {
-        const int8_t* p = a.cache.v + off + n * kKvPage + 16 * g;
-#pragma unroll
-        for (int j = 0; j < B; ++j) buf[h & 1][j] = *(const u32x4*)(p + 16 * ((h - H) * B + j) * kKvPage);
-      }
-    };
-    if (steps > 0) {
-      ask(0, 0);
-      ask(0, 1);
-    }
     for (int i = 0; i < steps; ++i) {
       // What follows part h in its buffer: part h + 2 of this page or the next one's.
       auto refill = [&](int h) {
@@ -342,6 +362,11 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
         }
         refill(H + h);
       }
+    }
+    base += 256;
+    if (base < end) {
+      ids(base);
+      start();
     }
   }
 #pragma unroll
