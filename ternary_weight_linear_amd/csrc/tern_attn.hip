@@ -29,6 +29,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "tern_device.h"
 #include "tern_internal.h"
 
@@ -116,28 +118,114 @@ __device__ __forceinline__ Pages pages_of(const KvAttnArgs& a, const Seq& s, int
   return p;
 }
 
-// Grid: (row block, kv head) x splits x seqs; 4 waves, wave w takes pages
-// w, w + 4, ... of the split's run.
+// A unit is one block of `plan.rows` query rows of a sequence, for one kv head.
+// Unit u of a head: sequence u / row_blocks, block u % row_blocks.
+struct Unit {
+  Seq seq;
+  int rows, r0, rlast;  // rows of the sequence, first and last of the unit (rlast < r0: none)
+  Pages pages;
+};
+__device__ __forceinline__ Unit unit_of(const KvAttnArgs& a, const KvAttnPlan& plan, int u) {
+  const int group = a.q_heads / a.cache.heads;
+  Unit x;
+  x.seq = sequence(a, u / plan.row_blocks);
+  x.rows = x.seq.n * group;
+  x.r0 = u % plan.row_blocks * plan.rows;
+  x.rlast = min(x.r0 + plan.rows, x.rows) - 1;
+  if (x.rlast >= x.r0)
+    x.pages = pages_of(a, x.seq, x.r0 / group, x.rlast / group);
+  else
+    x.pages = Pages{0, 0, 0, 0};
+  return x;
+}
+
+// Balanced runs (plan.runs > 0). The pages of all units of a head, one unit
+// after the other, are cut into runs of equal length, one a workgroup, so that
+// sequences of any lengths load the machine evenly; a run that ends inside a
+// unit leaves a partial result there, which the join kernel adds up. Lengths
+// are only known on the device, so every workgroup computes the prefix sums
+// of the units' pages itself, and the first leaves them for the join kernel:
+//   head of the workspace: run length, then pre[0 .. units];
+//   then partial sums [heads][runs][2][rows][D] and (maximum, sum) pairs
+//   [heads][runs][2][rows][2]; a run's slot 0 holds the unit that it enters
+//   in the middle, slot 1 the one that it begins and does not finish.
+struct Run {
+  int length, begin, end, unit;  // pages [begin, end) of the head, starting in `unit`
+};
+__device__ __forceinline__ Run make_runs(const KvAttnArgs& a, const KvAttnPlan& plan, int w, int* pre, int* ws) {
+  const int units = a.batch.seqs * plan.row_blocks;
+  const int per = (units + 255) >> 8, u0 = threadIdx.x * per;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int sum = 0;
+  for (int u = u0; u < min(u0 + per, units); ++u) {
+    const int c = unit_of(a, plan, u).pages.count;
+    pre[u + 1] = c;
+    sum += c;
+  }
+  int scan = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(scan, d);
+    if (lane >= d) scan += v;
+  }
+  int* tail = pre + units + 1;  // the four waves' sums, then the unit found
+  if (lane == 63) tail[wave] = scan;
+  __syncthreads();
+  int at = scan - sum;
+  for (int i = 0; i < wave; ++i) at += tail[i];
+  const int total = (tail[0] + tail[1]) + (tail[2] + tail[3]);
+  Run r;
+  r.length = max(plan.least, (total + plan.runs - 1) / plan.runs);
+  r.length = __builtin_amdgcn_readfirstlane(r.length);
+  r.begin = __builtin_amdgcn_readfirstlane((int)min((int64_t)w * r.length, (int64_t)total));
+  r.end = __builtin_amdgcn_readfirstlane((int)min((int64_t)r.begin + r.length, (int64_t)total));
+  if (threadIdx.x == 0) pre[0] = 0;
+  for (int u = u0; u < min(u0 + per, units); ++u) {
+    const int c = pre[u + 1];
+    if (at <= r.begin && r.begin < at + c) tail[4] = u;
+    at += c;
+    pre[u + 1] = at;
+  }
+  __syncthreads();
+  r.unit = __builtin_amdgcn_readfirstlane(tail[4]);
+  if (blockIdx.x == 0) {
+    for (int u = threadIdx.x; u <= units; u += blockDim.x) ws[1 + u] = pre[u];
+    if (threadIdx.x == 0) ws[0] = r.length;
+  }
+  return r;
+}
+__device__ __forceinline__ int64_t ws_head(const KvAttnArgs& a, const KvAttnPlan& plan) {  // in floats
+  return ((int64_t)a.batch.seqs * plan.row_blocks + 2 + 63) / 64 * 64;
+}
+
+// Grid: kv heads x units, or kv heads x runs. 4 waves; wave w takes pages w,
+// w + 4, ... of what the workgroup visits of a unit.
 template <int D, int NT>
-__global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 3 : D * NT <= 256 ? 2 : 1) tern_kv_attn_kernel(KvAttnArgs a, KvAttnPlan plan, float* part) {
+__global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
+    tern_kv_attn_kernel(KvAttnArgs a, KvAttnPlan plan, float* ws) {
   constexpr int C = D / 64;   // 64-wide chunks of a head
   constexpr int HT = D / 16;  // 16-wide row tiles of O^T
   constexpr int R = 16 * NT;
-  extern __shared__ float lds[];  // 2 x (R x D + 2 R): partial results of two waves
+  constexpr int kSlot = R * D + 2 * R;  // a wave's partial result
+  extern __shared__ float lds[];        // two of those; with runs, the prefix sums follow
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int heads = a.cache.heads, group = a.q_heads / heads;
-  const int head = blockIdx.x % heads, block = blockIdx.x / heads;
-  const int split = blockIdx.y, sid = blockIdx.z;
-  const Seq seq = sequence(a, sid);
-  const int rows = seq.n * group;
-  const int r0 = block * R;
-  if (r0 >= rows) return;
-  const int rlast = min(r0 + R, rows) - 1;
-  const Pages pages = pages_of(a, seq, r0 / group, rlast / group);
-  const int begin = split * plan.chunk, end = min(pages.count, begin + plan.chunk);
-  if (begin >= end && split > 0) return;
-  const int splits = (pages.count + plan.chunk - 1) / plan.chunk;  // of this row block
+  const int head = blockIdx.x % heads, w = blockIdx.x / heads;
+  const int* pre = (const int*)(lds + 2 * kSlot);
+  Run run{0, 0, 0, w};
+  if (plan.runs) {
+    run = make_runs(a, plan, w, (int*)(lds + 2 * kSlot), (int*)ws);
+    if (run.begin >= run.end) return;
+  }
+  for (int u = run.unit, from = run.begin;;) {
+  const Unit unit = unit_of(a, plan, u);
+  if (unit.rlast < unit.r0) return;  // only without runs: no pages, no run here
+  const Seq seq = unit.seq;
+  const Pages pages = unit.pages;
+  const int r0 = unit.r0, rows = unit.rows, rlast = unit.rlast;
+  const int begin = plan.runs ? __builtin_amdgcn_readfirstlane(from - pre[u]) : 0;
+  const int end = plan.runs ? min(pages.count, begin + run.end - from) : pages.count;
 
   // Page ids and scales of this wave's next 64 pages, one a lane; then keys
   // and values, asked for one buffer ahead of their use: a page's 16-byte
@@ -146,7 +234,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
   // non-temporal.
   constexpr int N = D / 16, B = N < 8 ? N : 8, H = N / B;
   u32x4 buf[2][B];
-  const int32_t* table = a.batch.page_table + (int64_t)sid * a.batch.table_width;
+  const int32_t* table = a.batch.page_table + (int64_t)(u / plan.row_blocks) * a.batch.table_width;
   int id = -1, steps = 0;
   float ks = 0.f, vs = 0.f;
   auto ids = [&](int base) {
@@ -164,30 +252,25 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
     }
   };
   // Part h (0..2H-1: keys, then values) of step i's page into its buffer. A
-  // page outside the cache reads page 0 instead, and is masked.
+  // page outside the cache, and one past the last step, are buffers of no
+  // bytes: they read as zeros and cost no traffic, and every step issues the
+  // same loads, so that a wait for one of them never waits for a later one.
   auto ask = [&](int i, int h) {
-    const int pid = max(__builtin_amdgcn_readlane(id, i), 0);
+    const int pid = i < steps ? __builtin_amdgcn_readlane(id, i) : -1;
     const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
-    if (h < H) {
-      const int8_t* p = a.cache.k + off + n * D + 16 * g;
+    const rsrc_t page = make_rsrc((h < H ? a.cache.k : a.cache.v) + off, pid < 0 ? 0 : kKvPage * D);
+    const int lane_at = h < H ? n * D + 16 * g : n * kKvPage + 16 * g;
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const int x = h * B + j;  // tokens 16 (x / C) .., elements 64 (x % C) ..
-        buf[h & 1][j] = __builtin_nontemporal_load((const u32x4*)(p + 16 * (x / C) * D + 64 * (x % C)));
-      }
-    } else {
-      const int8_t* p = a.cache.v + off + n * kKvPage + 16 * g;
-#pragma unroll
-      for (int j = 0; j < B; ++j)
-        buf[h & 1][j] = __builtin_nontemporal_load((const u32x4*)(p + 16 * ((h - H) * B + j) * kKvPage));
+    for (int j = 0; j < B; ++j) {
+      const int x = h % H * B + j;  // keys: tokens 16 (x / C) .., elements 64 (x % C) ..; values: elements 16 x ..
+      const int at = h < H ? 16 * (x / C) * D + 64 * (x % C) : 16 * x * kKvPage;
+      buf[h & 1][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(page, lane_at, at, kAuxNontemporal));
     }
   };
   auto start = [&]() {
     scales();
-    if (steps > 0) {
-      ask(0, 0);
-      ask(0, 1);
-    }
+    ask(0, 0);
+    ask(0, 1);
   };
   // The chain of dependent loads at the start (lengths, page ids, scales and
   // codes) is what a short call waits for: everything is asked for as soon as
@@ -258,7 +341,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
       auto refill = [&](int h) {
         if (h + 2 < 2 * H)
           ask(i, h + 2);
-        else if (i + 1 < steps)
+        else
           ask(i + 1, h + 2 - 2 * H);
       };
       const bool absent = __builtin_amdgcn_readlane(id, i) < 0;
@@ -299,18 +382,16 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
           float f = ksc * qs[t];
           f = f > kMostFactor ? kMostFactor : f;  // NaN stays
           float mx = kNone;
-          bool see[4][4];
 #pragma unroll
           for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if constexpr (decltype(masked)::value) {
                 const int j = j0 + 16 * b + 4 * g + e;
-                see[b][e] = !absent && j <= pos[t] && (!a.window || j > pos[t] - a.window || j < a.sinks);
-                mx = fmaxf(mx, see[b][e] ? s[t][b][e] : kNone);
-              } else {
-                mx = fmaxf(mx, s[t][b][e]);
+                const bool see = !absent && j <= pos[t] && (!a.window || j > pos[t] - a.window || j < a.sinks);
+                s[t][b][e] = see ? s[t][b][e] : kNone;
               }
+              mx = fmaxf(mx, s[t][b][e]);
             }
           mx = group_max(mx);
           const float top = mx == kNone ? kNone : __builtin_fmaf(mx, f, lvs);
@@ -326,7 +407,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][e], f, add));
-              if constexpr (decltype(masked)::value) p[e] = see[b][e] ? p[e] : 0.f;
+              if constexpr (decltype(masked)::value) p[e] = s[t][b][e] == kNone ? 0.f : p[e];  // also where f is NaN
               sum += p[e];
             }
             const u32x2 w = {pack_f16(p[0], p[1]), pack_f16(p[2], p[3])};
@@ -373,22 +454,20 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
   for (int t = 0; t < NT; ++t) L[t] = group_sum(L[t]);
 
   // Join the four waves: 2 and 3 into 0 and 1, then 1 into 0.
-  constexpr int kSlot = R * D + 2 * R;
 #pragma unroll
-  for (int from = 2; from >= 1; from >>= 1) {
-    const int slot = wave % from;
-    float* ml = lds + slot * kSlot + R * D;
-    if (wave >= from && wave < 2 * from) {
+  for (int half = 2; half >= 1; half >>= 1) {
+    float* slot = lds + wave % half * kSlot;
+    float* ml = slot + R * D;
+    if (wave >= half && wave < 2 * half) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int h = 0; h < HT; ++h)
-          *(f32x4*)(lds + slot * kSlot + ((t * HT + h) * 64 + lane) * 4) = o[t][h];
+        for (int h = 0; h < HT; ++h) *(f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) = o[t][h];
         if (g == 0) ml[16 * t + n] = M[t], ml[R + 16 * t + n] = L[t];
       }
     }
     __syncthreads();
-    if (wave < from) {
+    if (wave < half) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float m2 = ml[16 * t + n], l2 = ml[R + 16 * t + n];
@@ -398,73 +477,76 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D == 128 && NT == 1 ? 
         L[t] = L[t] * x + l2 * y;
 #pragma unroll
         for (int h = 0; h < HT; ++h)
-          o[t][h] = o[t][h] * x + *(const f32x4*)(lds + slot * kSlot + ((t * HT + h) * 64 + lane) * 4) * y;
+          o[t][h] = o[t][h] * x + *(const f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) * y;
       }
     }
     __syncthreads();
   }
-  if (wave != 0) return;
-  // Row of the lane in [tokens][q_heads], or -1 past the sequence's last.
-  auto row_at = [&](int t) -> int64_t {
-    const int r = r0 + 16 * t + n;
-    return r < rows ? (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group : -1;
-  };
-  if (splits <= 1) {
+  if (wave == 0) {
+    const bool whole = begin == 0 && end == pages.count;
+    const int64_t slot = ((int64_t)head * plan.runs + w) * 2 + (begin == 0);
+    float* po = ws + ws_head(a, plan) + slot * R * D;
+    float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * R * D + slot * R * 2;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int64_t at = row_at(t);
-      if (at < 0) continue;
-      const float inv = L[t] == 0.f ? 0.f : 1.0f / (L[t] * kPScale);
-      uint16_t* out = a.out + at * D + 4 * g;
+      const int r = r0 + 16 * t + n;
+      if (r >= rows) continue;
+      if (whole) {
+        const int64_t at = (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group;
+        const float inv = L[t] == 0.f ? 0.f : 1.0f / (L[t] * kPScale);
+        uint16_t* out = a.out + at * D + 4 * g;
 #pragma unroll
-      for (int h = 0; h < HT; ++h)
-        *(uint2*)(out + 16 * h) =
-            uint2{pack_bf16(o[t][h][0] * inv, o[t][h][1] * inv), pack_bf16(o[t][h][2] * inv, o[t][h][3] * inv)};
+        for (int h = 0; h < HT; ++h)
+          *(uint2*)(out + 16 * h) =
+              uint2{pack_bf16(o[t][h][0] * inv, o[t][h][1] * inv), pack_bf16(o[t][h][2] * inv, o[t][h][3] * inv)};
+      } else {
+#pragma unroll
+        for (int h = 0; h < HT; ++h) *(f32x4*)(po + (16 * t + n) * D + 16 * h + 4 * g) = o[t][h];
+        if (g == 0) *(float2*)(pm + (16 * t + n) * 2) = float2{M[t], L[t]};
+      }
     }
-    return;
   }
-  const int64_t all = (int64_t)a.tokens * a.q_heads;
-  float* po = part + (int64_t)split * all * D;
-  float* pm = part + (int64_t)plan.splits * all * D + (int64_t)split * all * 2;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t at = row_at(t);
-    if (at < 0) continue;
-#pragma unroll
-    for (int h = 0; h < HT; ++h) *(f32x4*)(po + at * D + 16 * h + 4 * g) = o[t][h];
-    if (g == 0) *(float2*)(pm + at * 2) = float2{M[t], L[t]};
+  if (!plan.runs) return;
+  from += end - begin;
+  if (from >= run.end) return;
+  do ++u;
+  while (pre[u + 1] == pre[u]);  // the next unit with pages: there is one before run.end
+  u = __builtin_amdgcn_readfirstlane(u);
   }
 }
 
-// Joins the runs of each row; one workgroup of 256 threads a row. Every
-// D/4 threads add the runs s, s + G, ... of four elements each, and the G
+// Joins the runs of a unit: one workgroup of 256 threads a row. Every D/4
+// threads add the pieces i, i + G, ... of four elements each, and the G
 // partial sums are added in order, so a row's result does not depend on timing.
 template <int D>
-__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* part) {
-  constexpr int G = 1024 / D;
-  __shared__ float weight[kKvMaxSplits];
+__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* ws) {
+  constexpr int G = 1024 / D, kMost = kKvMaxRuns / 256;
+  __shared__ float weight[kKvMaxRuns];
   __shared__ float red[8];
   __shared__ f32x4 sums[256];
   const int heads = a.cache.heads, group = a.q_heads / heads;
-  const Seq seq = sequence(a, blockIdx.z);
-  const int tok = blockIdx.x, h = blockIdx.y;
-  if (tok >= seq.n) return;
-  const int r0 = (tok * group + h % group) / plan.rows * plan.rows;
-  const int rlast = min(r0 + plan.rows, seq.n * group) - 1;
-  const Pages pages = pages_of(a, seq, r0 / group, rlast / group);
-  const int splits = (pages.count + plan.chunk - 1) / plan.chunk;
-  if (splits <= 1) return;  // written by its workgroup
-  const int64_t all = (int64_t)a.tokens * a.q_heads;
-  const int64_t at = (int64_t)(seq.row0 + tok) * a.q_heads + h;
-  const float2* pm = (const float2*)(part + (int64_t)plan.splits * all * D) + at;
+  const int head = blockIdx.x % heads, row = blockIdx.x / heads, u = blockIdx.y;
+  const int* pre = (const int*)ws + 1;
+  const int length = pre[-1], p0 = pre[u], p1 = pre[u + 1];
+  const Seq seq = sequence(a, u / plan.row_blocks);
+  const int r = u % plan.row_blocks * plan.rows + row;
+  if (r >= seq.n * group) return;
+  const int first = p0 / length, last = p1 > p0 ? (p1 - 1) / length : first - 1;
+  if (first == last) return;  // one piece: its workgroup wrote the result
+  const int pieces = last - first + 1;  // 0: the rows see nothing
+  const int64_t at = (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group;
+  // Piece i is in slot 0 of run first + i, but for the first one, in slot 1.
+  const int64_t slots = ((int64_t)head * plan.runs + first) * 2;
+  const float* po = ws + ws_head(a, plan) + (slots * plan.rows + row) * D;
+  const float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * plan.rows * D + (slots * plan.rows + row) * 2;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float M = kNone;
-  float2 ml[kKvMaxSplits / 256];
+  float2 ml[kMost];
 #pragma unroll
-  for (int u = 0; u < kKvMaxSplits / 256; ++u) {
-    const int s = threadIdx.x + 256 * u;
-    ml[u] = s < splits ? pm[s * all] : float2{kNone, 0.f};
-    M = fmaxf(M, ml[u].x);
+  for (int x = 0; x < kMost; ++x) {
+    const int i = threadIdx.x + 256 * x;
+    ml[x] = i < pieces ? *(const float2*)(pm + (int64_t)(i ? 2 * i : 1) * plan.rows * 2) : float2{kNone, 0.f};
+    M = fmaxf(M, ml[x].x);
   }
   for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
   if (lane == 0) red[wave] = M;
@@ -473,12 +555,12 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
   const float b = M == kNone ? 0.f : M;
   float L = 0.f;
 #pragma unroll
-  for (int u = 0; u < kKvMaxSplits / 256; ++u) {
-    const int s = threadIdx.x + 256 * u;
-    const float w = __builtin_amdgcn_exp2f(ml[u].x - b);
-    if (s < splits) {
-      weight[s] = w;
-      L = __builtin_fmaf(ml[u].y, w, L);
+  for (int x = 0; x < kMost; ++x) {
+    const int i = threadIdx.x + 256 * x;
+    const float y = __builtin_amdgcn_exp2f(ml[x].x - b);
+    if (i < pieces) {
+      weight[i] = y;
+      L = __builtin_fmaf(ml[x].y, y, L);
     }
   }
   L = wave_sum(L);
@@ -486,10 +568,10 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
   __syncthreads();
   L = (red[4] + red[5]) + (red[6] + red[7]);
   const int e = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
-  const f32x4* po = (const f32x4*)(part + at * D) + e;
   f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int s = grp; s < splits; s += G) o += po[s * all * (D / 4)] * weight[s];
+  for (int i = grp; i < pieces; i += G)
+    o += *(const f32x4*)(po + (int64_t)(i ? 2 * i : 1) * plan.rows * D + 4 * e) * weight[i];
   sums[threadIdx.x] = o;
   __syncthreads();
   if (grp != 0) return;
@@ -500,23 +582,25 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
 }
 
 template <int D, int NT>
-hipError_t go(const KvAttnArgs& a, const KvAttnPlan& p, float* part, hipStream_t st) {
-  constexpr int lds = 2 * (16 * NT * D + 2 * 16 * NT) * 4;
+hipError_t go(const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) {
+  const int units = a.batch.seqs * p.row_blocks;
+  const int lds = 2 * (16 * NT * D + 2 * 16 * NT) * 4 + (p.runs ? (units + 6) * 4 : 0);
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute((const void*)tern_kv_attn_kernel<D, NT>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  tern_kv_attn_kernel<D, NT><<<dim3(p.row_blocks * a.cache.heads, p.splits, a.batch.seqs), dim3(256), lds, st>>>(a, p, part);
+  tern_kv_attn_kernel<D, NT><<<dim3(a.cache.heads * (p.runs ? p.runs : units)), dim3(256), lds, st>>>(a, p, ws);
   return hipGetLastError();
 }
 
 template <int D>
-int launch(const KvAttnArgs& a, const KvAttnPlan& p, float* part, hipStream_t st) {
-  const hipError_t e = p.rows == 16 ? go<D, 1>(a, p, part, st) : go<D, 2>(a, p, part, st);
+int launch(const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) {
+  const hipError_t e = p.rows == 16 ? go<D, 1>(a, p, ws, st) : go<D, 2>(a, p, ws, st);
   if (kernel_launched((int)e, TERN_KERNEL_KV_ATTN)) return (int)e;
-  if (p.splits == 1) return 0;
-  tern_kv_attn_join_kernel<D><<<dim3(a.batch.max_q, a.q_heads, a.batch.seqs), dim3(256), 0, st>>>(a, p, part);
+  if (!p.runs) return 0;
+  const int rows = std::min(p.rows, a.q_heads / a.cache.heads * a.batch.max_q);
+  tern_kv_attn_join_kernel<D><<<dim3(rows * a.cache.heads, a.batch.seqs * p.row_blocks), dim3(256), 0, st>>>(a, p, ws);
   return kernel_launched((int)hipGetLastError(), TERN_KERNEL_KV_ATTN_JOIN);
 }
 

@@ -163,24 +163,33 @@ int64_t attn_pages(const tern::KvAttnArgs& a, int tokens_of_block) {
   return std::min(all, seen);
 }
 
+constexpr int kComputeUnits = 256;  // of the part that this library is built for
+
 tern::KvAttnPlan plan_attn(const tern::KvAttnArgs& a) {
   tern::KvAttnPlan p{};
   const int64_t group = a.q_heads / a.cache.heads, rows = group * a.batch.max_q;
   p.rows = rows <= 16 ? 16 : 32;
   p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
   const int64_t pages = attn_pages(a, std::min<int64_t>(a.batch.max_q, (p.rows + group - 2) / group + 1));
-  // About three workgroups a CU, and at least two pages for each of their four waves.
-  const int64_t blocks = (int64_t)p.row_blocks * a.cache.heads * a.batch.seqs;
-  const int64_t want = std::max<int64_t>(1, 768 / blocks);
-  p.chunk = (int)std::max<int64_t>(8, (pages + want - 1) / want);
-  p.splits = (int)((pages + p.chunk - 1) / p.chunk);
+  const int64_t units = (int64_t)p.row_blocks * a.batch.seqs;
+  // Fewer than two workgroups a compute unit would leave the machine waiting
+  // for the longest of them: then one run a compute unit, of equal lengths.
+  // One workgroup with its loads in flight fills a unit's share of the memory
+  // (256 / 320 / 512 / 768 runs: 64 / 83 / 68 / 72 us for 32 sequences of 1024
+  // to 8192 tokens, 51 / 68 / 57 / 62 us for one of 131072; a workgroup a unit:
+  // 71 us and 875 us); with two units each, 512 of equal lengths, runs and the
+  // second kernel only cost (54 us, against 46 us without).
+  p.least = 8;
+  if (pages > p.least && units <= tern::kKvMaxUnits && units * a.cache.heads < 2 * kComputeUnits)
+    p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({kComputeUnits / a.cache.heads, units * pages / p.least, tern::kKvMaxRuns}));
   return p;
 }
 
-// fp32 per (split, row): the weighted sum of values, the running maximum and the sum.
+// fp32 words: run length and prefix sums, then two slots a run of partial sums, maximum and sum of each row.
 size_t attn_ws(const tern::KvAttnArgs& a, const tern::KvAttnPlan& p) {
-  if (p.splits <= 1) return 0;
-  return (size_t)p.splits * a.tokens * a.q_heads * (a.cache.dim + 2) * sizeof(float);
+  if (!p.runs) return 0;
+  const size_t head = ((size_t)a.batch.seqs * p.row_blocks + 2 + 63) / 64 * 64;
+  return (head + (size_t)a.cache.heads * p.runs * 2 * p.rows * (a.cache.dim + 2)) * sizeof(float);
 }
 
 }  // namespace
@@ -209,7 +218,7 @@ tern_status tern_kv_attn(const tern_kv_cache* cache, const tern_kv_batch* batch,
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_ERR_WORKSPACE, "tern_kv_attn needs %zu bytes of workspace, got %zu", need, ws ? ws_bytes : (size_t)0);
   if (need && !aligned16(ws)) return fail(TERN_ERR_ALIGN, "the workspace must be 16-byte aligned");
-  if ((int64_t)p.row_blocks * a.cache.heads > kMaxGrid || p.splits > tern::kKvMaxSplits)
+  if ((int64_t)p.row_blocks * a.cache.heads * a.batch.seqs > kMaxGrid)
     return fail(TERN_ERR_SHAPE, "tern_kv_attn: too many rows or pages for one launch");
   if (!tern::launch_kv_attn) return no_unit();
   a.q = (const uint16_t*)q_bf16, a.out = (uint16_t*)out_bf16, a.q_stride = q_stride, a.scale = scale;

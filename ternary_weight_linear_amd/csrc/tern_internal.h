@@ -267,13 +267,16 @@ struct KvAttnArgs {
   int tokens, q_heads, window, sinks;
   float scale;
 };
-// Launch shape of the attention: row blocks of `rows` (token, head of the
-// group) rows per kv head, and the visible pages cut into `splits` runs of
-// `chunk` pages (joined by a second kernel when splits > 1).
+// Launch shape of the attention: units of `rows` (token, head of the group)
+// rows per kv head, `row_blocks` a sequence. runs 0: one workgroup a unit.
+// runs > 0: the pages of a head's units cut into that many runs of equal
+// length (at least `least` pages), one a workgroup, and joined by a second
+// kernel.
 struct KvAttnPlan {
-  int rows, row_blocks, splits, chunk;
+  int rows, row_blocks, runs, least;
 };
-constexpr int kKvMaxSplits = 1024;
+constexpr int kKvMaxRuns = 256;    // per head
+constexpr int kKvMaxUnits = 2048;  // with runs: their prefix sums are in LDS
 TERN_WEAK int launch_kv_attn(const KvAttnArgs& a, const KvAttnPlan& p, void* ws, void* stream);
 
 }  // namespace tern
