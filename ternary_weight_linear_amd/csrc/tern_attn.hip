@@ -198,6 +198,135 @@ __device__ __forceinline__ int64_t ws_head(const KvAttnArgs& a, const KvAttnPlan
   return ((int64_t)a.batch.seqs * plan.row_blocks + 2 + 63) / 64 * 64;
 }
 
+// Query rows of a wave: NT tiles of 16, lane & 15 the row of each.
+template <int D, int NT>
+struct Queries {
+  static constexpr int C = D / 64;  // 64-wide chunks of a head
+  u32x4 raw[NT][C][2];
+  f16x8 op[NT][C][2];  // operands: elements 64 c + 16 g + 8 k ..
+  float factor[NT];    // from a product of operands and codes to a score in powers of two, but for the key scale
+  int pos[NT];         // the row's position
+
+  // Asks for the rows from `row` of a sequence on; rows past its last repeat that.
+  __device__ __forceinline__ void ask(const KvAttnArgs& a, const Seq& seq, int row, int rows, int head, int group, int n, int g) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int rr = min(row + 16 * t + n, rows - 1);
+      const int tok = rr / group, h = head * group + rr % group;
+      pos[t] = seq.kv - seq.n + tok;
+      const uint16_t* q = a.q + (int64_t)(seq.row0 + tok) * a.q_stride + (int64_t)h * D;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) raw[t][c][k] = *(const u32x4*)(q + 64 * c + 16 * g + 8 * k);
+    }
+  }
+  // fp16 operands, each row brought to [1, 2) by a power of two.
+  __device__ __forceinline__ void make(float scale) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m = max(m, max((raw[t][c][k][i] << 16) & 0x7fff0000u, raw[t][c][k][i] & 0x7fff0000u));
+      m = __float_as_uint(group_max(__uint_as_float(min(m, 0x7f800000u))));  // a NaN takes infinity's exponent
+      // 2^e <= max|q| < 2^(e+1); rows of zeros and of subnormals take e = -126
+      const int e = min(max((int)(m >> 23) - 127, -126), 126);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      factor[t] = scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            op[t][c][k][2 * i] = (_Float16)(bf16_lo(raw[t][c][k][i]) * down);
+            op[t][c][k][2 * i + 1] = (_Float16)(bf16_hi(raw[t][c][k][i]) * down);
+          }
+    }
+  }
+};
+
+// What a page multiplies with: key scale, log2 of the value scale w and
+// 2^-15 / w; a page outside the cache is absent.
+struct PageScales {
+  float k, log_v, inv_v;
+  bool absent;
+};
+
+// Softmax of a page's scores s for the 16 rows of one tile: running maximum M
+// and sum L, the factor alpha for what was summed before, and the second
+// product's operands p. MASKED: some row does not see the whole page.
+template <bool MASKED>
+__device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w, float factor, int pos, int j0, int g,
+                                             int window, int sinks, float& M, float& L, float& alpha, f16x8 (&p)[2]) {
+  float f = w.k * factor;
+  f = f > kMostFactor ? kMostFactor : f;  // NaN stays
+  float mx = kNone;
+  // Masked: element 16 b + e of this lane's tokens is seen up to `last`, but
+  // for those from `hide` on and before `show` (past the sinks, before the window).
+  const int at = j0 + 4 * g;
+  const int last = w.absent ? -1 : pos - at, show = window ? pos - window + 1 - at : 0, hide = window ? sinks - at : 64;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (MASKED) {
+        const int x = 16 * b + e;
+        s[b][e] = x > last || (x >= hide && x < show) ? kNone : s[b][e];
+      }
+      mx = fmaxf(mx, s[b][e]);
+    }
+  mx = group_max(mx);
+  const float top = mx == kNone ? kNone : __builtin_fmaf(mx, f, w.log_v);
+  const float Mn = fmaxf(M, top);
+  const float base = Mn == kNone ? 0.f : Mn;
+  alpha = __builtin_amdgcn_exp2f(M - base);
+  M = Mn;
+  const float add = (w.log_v - base) + 15.f;  // p' in fp16 stands times 2^15
+  float sum = 0.f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], f, add));
+      if constexpr (MASKED) x[e] = s[b][e] == kNone ? 0.f : x[e];  // also where f is NaN
+      sum += x[e];
+    }
+    const u32x2 h = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3])};
+    const f16x4 v = __builtin_bit_cast(f16x4, h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[b >> 1][4 * (b & 1) + e] = v[e];
+  }
+  L = __builtin_fmaf(L, alpha, sum * w.inv_v);
+}
+
+__device__ __forceinline__ float lane_float(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
+// A row's result, or its partial sums, from the lanes that hold it (four
+// consecutive elements of every 16).
+template <int D>
+__device__ __forceinline__ void write_row(const KvAttnArgs& a, const f32x4 (&o)[D / 16], float L, int64_t at, int g) {
+  const float inv = L == 0.f ? 0.f : 1.0f / (L * kPScale);
+  uint16_t* out = a.out + at * D + 4 * g;
+#pragma unroll
+  for (int h = 0; h < D / 16; ++h)
+    *(uint2*)(out + 16 * h) = uint2{pack_bf16(o[h][0] * inv, o[h][1] * inv), pack_bf16(o[h][2] * inv, o[h][3] * inv)};
+}
+template <int D>
+__device__ __forceinline__ void write_part(float* po, float* pm, const f32x4 (&o)[D / 16], float M, float L, int row, int g) {
+#pragma unroll
+  for (int h = 0; h < D / 16; ++h) *(f32x4*)(po + row * D + 16 * h + 4 * g) = o[h];
+  if (g == 0) *(float2*)(pm + row * 2) = float2{M, L};
+}
+
 // Grid: kv heads x units, or kv heads x runs. 4 waves; wave w takes pages w,
 // w + 4, ... of what the workgroup visits of a unit.
 template <int D, int NT>
@@ -276,51 +405,12 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
   // codes) is what a short call waits for: everything is asked for as soon as
   // its address is known, the query rows between the ids and the codes.
   ids(begin);
-  u32x4 raw[NT][C][2];
-  int pos[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int rr = min(r0 + 16 * t + n, rows - 1);
-    const int tok = rr / group, h = head * group + rr % group;
-    pos[t] = seq.kv - seq.n + tok;
-    const uint16_t* q = a.q + (int64_t)(seq.row0 + tok) * a.q_stride + (int64_t)h * D;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) raw[t][c][k] = *(const u32x4*)(q + 64 * c + 16 * g + 8 * k);
-  }
+  Queries<D, NT> q;
+  q.ask(a, seq, r0, rows, head, group, n, g);
   __builtin_amdgcn_sched_barrier(0);
   start();
   __builtin_amdgcn_sched_barrier(0);
-
-  // The query rows as fp16 operands, each brought to [1, 2) by a power of two.
-  f16x8 qf[NT][C][2];
-  float qs[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m = max(m, max((raw[t][c][k][i] << 16) & 0x7fff0000u, raw[t][c][k][i] & 0x7fff0000u));
-    m = __float_as_uint(group_max(__uint_as_float(min(m, 0x7f800000u))));  // a NaN takes infinity's exponent
-    // 2^e <= max|q| < 2^(e+1); rows of zeros and of subnormals take e = -126
-    const int e = min(max((int)(m >> 23) - 127, -126), 126);
-    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-    qs[t] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          qf[t][c][k][2 * i] = (_Float16)(bf16_lo(raw[t][c][k][i]) * down);
-          qf[t][c][k][2 * i + 1] = (_Float16)(bf16_hi(raw[t][c][k][i]) * down);
-        }
-  }
+  q.make(a.scale);
   const int pos_min = seq.kv - seq.n + r0 / group, pos_max = seq.kv - seq.n + rlast / group;
 
   f32x4 o[NT][HT];
@@ -344,10 +434,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
         else
           ask(i + 1, h + 2 - 2 * H);
       };
-      const bool absent = __builtin_amdgcn_readlane(id, i) < 0;
-      const float ksc = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(ks), i));
-      const float lvs = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(lv), i));
-      const float ivs = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(iv), i));
+      const PageScales w{lane_float(ks, i), lane_float(lv, i), lane_float(iv, i), __builtin_amdgcn_readlane(id, i) < 0};
       const int j0 = pages.at(base + wave + 4 * i) * kKvPage;
 
       f32x4 s[NT][4];
@@ -360,63 +447,27 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < B; ++j) {
           const int x = h * B + j, b = x / C, c = x % C;
-          const u32x4 w = buf[h & 1][j];
-          const f16x8 k0 = codes8(w[0], w[1]), k1 = codes8(w[2], w[3]);
+          const u32x4 x16 = buf[h & 1][j];
+          const f16x8 k0 = codes8(x16[0], x16[1]), k1 = codes8(x16[2], x16[3]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, qf[t][c][0], s[t][b], 0, 0, 0);
-            s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, qf[t][c][1], s[t][b], 0, 0, 0);
+            s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q.op[t][c][0], s[t][b], 0, 0, 0);
+            s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q.op[t][c][1], s[t][b], 0, 0, 0);
           }
         }
         refill(h);
       }
 
       // Whether every row sees the whole page.
-      const bool whole = !absent && j0 + kKvPage - 1 <= pos_min &&
+      const bool whole = !w.absent && j0 + kKvPage - 1 <= pos_min &&
                          (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
       f16x8 pf[NT][2];
       float alpha[NT];
       auto softmax = [&](auto masked) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float f = ksc * qs[t];
-          f = f > kMostFactor ? kMostFactor : f;  // NaN stays
-          float mx = kNone;
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (decltype(masked)::value) {
-                const int j = j0 + 16 * b + 4 * g + e;
-                const bool see = !absent && j <= pos[t] && (!a.window || j > pos[t] - a.window || j < a.sinks);
-                s[t][b][e] = see ? s[t][b][e] : kNone;
-              }
-              mx = fmaxf(mx, s[t][b][e]);
-            }
-          mx = group_max(mx);
-          const float top = mx == kNone ? kNone : __builtin_fmaf(mx, f, lvs);
-          const float Mn = fmaxf(M[t], top);
-          const float base2 = Mn == kNone ? 0.f : Mn;
-          alpha[t] = __builtin_amdgcn_exp2f(M[t] - base2);
-          M[t] = Mn;
-          const float add = (lvs - base2) + 15.f;  // p' in fp16 stands times 2^15
-          float sum = 0.f;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            float p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][b][e], f, add));
-              if constexpr (decltype(masked)::value) p[e] = s[t][b][e] == kNone ? 0.f : p[e];  // also where f is NaN
-              sum += p[e];
-            }
-            const u32x2 w = {pack_f16(p[0], p[1]), pack_f16(p[2], p[3])};
-            const f16x4 v = __builtin_bit_cast(f16x4, w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pf[t][b >> 1][4 * (b & 1) + e] = v[e];
-          }
-          L[t] = __builtin_fmaf(L[t], alpha[t], sum * ivs);
-        }
+        for (int t = 0; t < NT; ++t)
+          page_softmax<decltype(masked)::value>(s[t], w, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
+                                                alpha[t], pf[t]);
       };
       if (whole)
         softmax(std::false_type{});
@@ -433,8 +484,8 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
 #pragma unroll
         for (int j = 0; j < B; ++j) {
           const int x = h * B + j;
-          const u32x4 w = buf[(H + h) & 1][j];
-          const f16x8 v0 = codes8(w[0], w[1]), v1 = codes8(w[2], w[3]);
+          const u32x4 x16 = buf[(H + h) & 1][j];
+          const f16x8 v0 = codes8(x16[0], x16[1]), v1 = codes8(x16[2], x16[3]);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][x], 0, 0, 0);
@@ -491,19 +542,10 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
     for (int t = 0; t < NT; ++t) {
       const int r = r0 + 16 * t + n;
       if (r >= rows) continue;
-      if (whole) {
-        const int64_t at = (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group;
-        const float inv = L[t] == 0.f ? 0.f : 1.0f / (L[t] * kPScale);
-        uint16_t* out = a.out + at * D + 4 * g;
-#pragma unroll
-        for (int h = 0; h < HT; ++h)
-          *(uint2*)(out + 16 * h) =
-              uint2{pack_bf16(o[t][h][0] * inv, o[t][h][1] * inv), pack_bf16(o[t][h][2] * inv, o[t][h][3] * inv)};
-      } else {
-#pragma unroll
-        for (int h = 0; h < HT; ++h) *(f32x4*)(po + (16 * t + n) * D + 16 * h + 4 * g) = o[t][h];
-        if (g == 0) *(float2*)(pm + (16 * t + n) * 2) = float2{M[t], L[t]};
-      }
+      if (whole)
+        write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g);
+      else
+        write_part<D>(po, pm, o[t], M[t], L[t], 16 * t + n, g);
     }
   }
   if (!plan.runs) return;
@@ -515,17 +557,213 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
   }
 }
 
-// Joins the runs of a unit: one workgroup of 256 threads a row. Every D/4
-// threads add the pieces i, i + G, ... of four elements each, and the G
-// partial sums are added in order, so a row's result does not depend on timing.
+// Many query rows: a unit of 128 rows, 32 a wave, whose waves share each
+// page's codes. The workgroup turns the codes into fp16 operands once, in LDS
+// (one page ahead: two buffers, one barrier a page), so that the conversion
+// costs a quarter of what it costs a wave by itself; the operands lie in the
+// order in which the lanes read them (64 lanes x 16 bytes each), free of bank
+// conflicts both ways.
 template <int D>
-__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* ws) {
-  constexpr int G = 1024 / D, kMost = kKvMaxRuns / 256;
-  __shared__ float weight[kKvMaxRuns];
-  __shared__ float red[8];
-  __shared__ f32x4 sums[256];
+__global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kernel(KvAttnArgs a, KvAttnPlan plan, float* ws) {
+  constexpr int NT = 2, R = 128;
+  constexpr int C = D / 64, HT = D / 16;
+  constexpr int N = D / 16;           // 16-byte loads of a page's keys, or values, by one wave
+  constexpr int kPage = 2 * N * 128;  // u32x4 of a buffer: keys, then values, two operands a load
+  extern __shared__ u32x4 tiles[];    // two buffers; with runs, the prefix sums follow
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
   const int heads = a.cache.heads, group = a.q_heads / heads;
-  const int head = blockIdx.x % heads, row = blockIdx.x / heads, u = blockIdx.y;
+  const int head = blockIdx.x % heads, w = blockIdx.x / heads;
+  int* const pre = (int*)(tiles + 2 * kPage);
+  Run run{0, 0, 0, a.batch.seqs * plan.row_blocks - 1 - w};  // without runs: the last rows, which see most, first
+  if (plan.runs) {
+    run = make_runs(a, plan, w, pre, (int*)ws);
+    if (run.begin >= run.end) return;
+  }
+  for (int u = run.unit, from = run.begin;;) {
+    const Unit unit = unit_of(a, plan, u);
+    if (unit.rlast < unit.r0) return;  // only without runs: no pages, no run here
+    const Seq seq = unit.seq;
+    const Pages pages = unit.pages;
+    const int rows = unit.rows, r0 = unit.r0 + 32 * wave;  // the wave's own rows from here on
+    const int begin = plan.runs ? __builtin_amdgcn_readfirstlane(from - pre[u]) : 0;
+    const int end = plan.runs ? min(pages.count, begin + run.end - from) : pages.count;
+
+    Queries<D, NT> q;
+    q.ask(a, seq, r0, rows, head, group, n, g);
+    const int32_t* table = a.batch.page_table + (int64_t)(u / plan.row_blocks) * a.batch.table_width;
+    // Ids and scales of 64 pages, one a lane; 62 steps are taken with them,
+    // since codes are asked for two pages ahead.
+    int id = -1;
+    float ks = 0.f, lv = 0.f, iv = 0.f;
+    auto ids = [&](int base) {
+      const int mine = base + lane;
+      id = mine < end ? table[pages.at(mine)] : -1;
+      if (id >= a.cache.pages) id = -1;
+      float vs = 0.f;
+      ks = 0.f;
+      if (id >= 0) {
+        const int64_t ph = (int64_t)id * heads + head;
+        ks = a.cache.k_scale[ph];
+        vs = a.cache.v_scale[ph];
+      }
+      vs = vs < kLeastScale ? kLeastScale : vs;
+      lv = __builtin_amdgcn_logf(vs);
+      iv = 1.0f / (vs * kPScale);
+    };
+    // The wave's quarter of a page's codes: loads wave, wave + 4, ... of keys
+    // and of values. A page that is absent, or past the end, reads as zeros.
+    u32x4 raw[2][N / 4];
+    auto ask = [&](int i) {
+      const int pid = __builtin_amdgcn_readlane(id, i);
+      const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
+      const rsrc_t kr = make_rsrc(a.cache.k + off, pid < 0 ? 0 : kKvPage * D);
+      const rsrc_t vr = make_rsrc(a.cache.v + off, pid < 0 ? 0 : kKvPage * D);
+#pragma unroll
+      for (int j = 0; j < N / 4; ++j) {
+        const int x = wave + 4 * j;
+        raw[0][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, n * D + 16 * g, 16 * (x / C) * D + 64 * (x % C), 0));
+        raw[1][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, n * kKvPage + 16 * g, 16 * x * kKvPage, 0));
+      }
+    };
+    auto convert = [&](u32x4* to) {
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+          const u32x4 c = raw[kv][j];
+          u32x4* o = to + (kv * N + wave + 4 * j) * 128 + lane;
+          o[0] = __builtin_bit_cast(u32x4, codes8(c[0], c[1]));
+          o[64] = __builtin_bit_cast(u32x4, codes8(c[2], c[3]));
+        }
+    };
+    ids(begin);
+    ask(0);
+    q.make(a.scale);
+    const int wlast = min(r0 + 31, rows - 1);
+    const int pos_min = seq.kv - seq.n + min(r0, rows - 1) / group, pos_max = seq.kv - seq.n + wlast / group;
+
+    f32x4 o[NT][HT];
+    float M[NT], L[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      M[t] = kNone;
+      L[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < HT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    convert(tiles);
+    ask(1);
+    int buffer = 0, base = begin;
+    for (int i = begin; i < end; ++i) {
+      if (i - base == 62) {
+        base = i;
+        ids(base);  // codes of page i + 1 are already on their way
+      }
+      const int at = i - base;
+      __syncthreads();  // this page's operands are written, and the other buffer is read
+      convert(tiles + (buffer ^ 1) * kPage);
+      ask(at + 2);
+      const u32x4* page = tiles + buffer * kPage + lane;
+      buffer ^= 1;
+      const PageScales ps{lane_float(ks, at), lane_float(lv, at), lane_float(iv, at), __builtin_amdgcn_readlane(id, at) < 0};
+      const int j0 = pages.at(i) * kKvPage;
+      // Pages that none of the wave's rows sees: after its last position, or
+      // past the sinks and before its first window.
+      if (r0 >= rows || ps.absent || j0 > pos_max ||
+          (a.window && j0 + kKvPage - 1 <= pos_min - a.window && j0 >= a.sinks))
+        continue;
+
+      f32x4 s[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) s[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // Operands are read A loads ahead of their products, the first values'
+      // before the softmax.
+      constexpr int A = 4;
+      f16x8 f[A][2];
+      auto read = [&](int x) {
+        f[x % A][0] = __builtin_bit_cast(f16x8, page[x * 128]);
+        f[x % A][1] = __builtin_bit_cast(f16x8, page[x * 128 + 64]);
+      };
+#pragma unroll
+      for (int x = 0; x < A; ++x) read(x);
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          s[t][x / C] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x % A][0], q.op[t][x % C][0], s[t][x / C], 0, 0, 0);
+          s[t][x / C] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x % A][1], q.op[t][x % C][1], s[t][x / C], 0, 0, 0);
+        }
+        read(x + A);
+      }
+      const bool whole = j0 + kKvPage - 1 <= pos_min &&
+                         (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
+      f16x8 pf[NT][2];
+      float alpha[NT];
+      auto softmax = [&](auto masked) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          page_softmax<decltype(masked)::value>(s[t], ps, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
+                                                alpha[t], pf[t]);
+      };
+      if (whole)
+        softmax(std::false_type{});
+      else
+        softmax(std::true_type{});
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (__any(alpha[t] != 1.f)) {  // a maximum moved (or a row is NaN)
+#pragma unroll
+          for (int x = 0; x < HT; ++x) o[t][x] *= alpha[t];
+        }
+#pragma unroll
+      for (int x = 0; x < HT; ++x) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x % A][0], pf[t][0], o[t][x], 0, 0, 0);
+          o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[x % A][1], pf[t][1], o[t][x], 0, 0, 0);
+        }
+        if (x + A < N) read(N + x + A);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) L[t] = group_sum(L[t]);
+
+    const bool whole = begin == 0 && end == pages.count;
+    const int64_t slot = ((int64_t)head * plan.runs + w) * 2 + (begin == 0);
+    float* po = ws + ws_head(a, plan) + slot * R * D;
+    float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * R * D + slot * R * 2;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = r0 + 16 * t + n;
+      if (r >= rows) continue;
+      if (whole)
+        write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g);
+      else
+        write_part<D>(po, pm, o[t], M[t], L[t], 32 * wave + 16 * t + n, g);
+    }
+    if (!plan.runs) return;
+    from += end - begin;
+    if (from >= run.end) return;
+    do ++u;
+    while (pre[u + 1] == pre[u]);  // the next unit with pages: there is one before run.end
+    u = __builtin_amdgcn_readfirstlane(u);
+    __syncthreads();  // the last page's operands are read
+  }
+}
+
+// Joins the runs of a unit, one wave a row: its lanes hold D / 64 elements
+// each and add the pieces in order.
+template <int D>
+__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* ws, int waves) {
+  constexpr int E = D / 64, kMost = kKvMaxRuns / 64;
+  const int heads = a.cache.heads, group = a.q_heads / heads;
+  const int lane = threadIdx.x & 63;
+  const int i = __builtin_amdgcn_readfirstlane((blockIdx.x * 256 + threadIdx.x) >> 6);  // (row, head) of the unit
+  if (i >= waves) return;
+  const int head = i % heads, row = i / heads, u = blockIdx.y;
   const int* pre = (const int*)ws + 1;
   const int length = pre[-1], p0 = pre[u], p1 = pre[u + 1];
   const Seq seq = sequence(a, u / plan.row_blocks);
@@ -533,74 +771,77 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
   if (r >= seq.n * group) return;
   const int first = p0 / length, last = p1 > p0 ? (p1 - 1) / length : first - 1;
   if (first == last) return;  // one piece: its workgroup wrote the result
-  const int pieces = last - first + 1;  // 0: the rows see nothing
+  const int pieces = last - first + 1;  // 0: the row sees nothing
   const int64_t at = (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group;
   // Piece i is in slot 0 of run first + i, but for the first one, in slot 1.
   const int64_t slots = ((int64_t)head * plan.runs + first) * 2;
-  const float* po = ws + ws_head(a, plan) + (slots * plan.rows + row) * D;
+  const float* po = ws + ws_head(a, plan) + (slots * plan.rows + row) * D + lane * E;
   const float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * plan.rows * D + (slots * plan.rows + row) * 2;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float M = kNone;
   float2 ml[kMost];
+  float M = kNone;
 #pragma unroll
   for (int x = 0; x < kMost; ++x) {
-    const int i = threadIdx.x + 256 * x;
-    ml[x] = i < pieces ? *(const float2*)(pm + (int64_t)(i ? 2 * i : 1) * plan.rows * 2) : float2{kNone, 0.f};
+    const int p = lane + 64 * x;
+    ml[x] = p < pieces ? *(const float2*)(pm + (int64_t)(p ? 2 * p : 1) * plan.rows * 2) : float2{kNone, 0.f};
     M = fmaxf(M, ml[x].x);
   }
   for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
-  if (lane == 0) red[wave] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float b = M == kNone ? 0.f : M;
   float L = 0.f;
 #pragma unroll
   for (int x = 0; x < kMost; ++x) {
-    const int i = threadIdx.x + 256 * x;
-    const float y = __builtin_amdgcn_exp2f(ml[x].x - b);
-    if (i < pieces) {
-      weight[i] = y;
-      L = __builtin_fmaf(ml[x].y, y, L);
-    }
+    ml[x].x = __builtin_amdgcn_exp2f(ml[x].x - b);
+    L = __builtin_fmaf(ml[x].y, ml[x].x, L);
   }
   L = wave_sum(L);
-  if (lane == 0) red[4 + wave] = L;
-  __syncthreads();
-  L = (red[4] + red[5]) + (red[6] + red[7]);
-  const int e = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int i = grp; i < pieces; i += G)
-    o += *(const f32x4*)(po + (int64_t)(i ? 2 * i : 1) * plan.rows * D + 4 * e) * weight[i];
-  sums[threadIdx.x] = o;
-  __syncthreads();
-  if (grp != 0) return;
+  float o[E] = {};
 #pragma unroll
-  for (int x = 1; x < G; ++x) o += sums[e + x * (D / 4)];
+  for (int x = 0; x < kMost; ++x) {
+    const int most = min(pieces - 64 * x, 64);
+    for (int p0 = 0; p0 < most; p0 += 8) {  // eight loads at a time; past the last, that one again with no weight
+      float f[8][E];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = min(p0 + j, most - 1) + 64 * x;
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[j][e] = po[(int64_t)(p ? 2 * p : 1) * plan.rows * D + e];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = p0 + j < most ? lane_float(ml[x].x, p0 + j) : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(f[j][e], y, o[e]);
+      }
+    }
+  }
   const float inv = L == 0.f ? 0.f : 1.0f / (L * kPScale);
-  *(uint2*)(a.out + at * D + 4 * e) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+  uint16_t* out = a.out + at * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e] * inv, 0.f);
 }
 
-template <int D, int NT>
-hipError_t go(const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) {
+template <class K>
+hipError_t go(K* kernel, int lds, const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) {
   const int units = a.batch.seqs * p.row_blocks;
-  const int lds = 2 * (16 * NT * D + 2 * 16 * NT) * 4 + (p.runs ? (units + 6) * 4 : 0);
+  if (p.runs) lds += (units + 6) * 4;
   if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute((const void*)tern_kv_attn_kernel<D, NT>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  tern_kv_attn_kernel<D, NT><<<dim3(a.cache.heads * (p.runs ? p.runs : units)), dim3(256), lds, st>>>(a, p, ws);
+  kernel<<<dim3(a.cache.heads * (p.runs ? p.runs : units)), dim3(256), lds, st>>>(a, p, ws);
   return hipGetLastError();
 }
 
 template <int D>
 int launch(const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) {
-  const hipError_t e = p.rows == 16 ? go<D, 1>(a, p, ws, st) : go<D, 2>(a, p, ws, st);
-  if (kernel_launched((int)e, TERN_KERNEL_KV_ATTN)) return (int)e;
+  auto few = [](int rows) { return 2 * (rows * D + 2 * rows) * 4; };
+  const hipError_t e = p.rows == 16   ? go(tern_kv_attn_kernel<D, 1>, few(16), a, p, ws, st)
+                       : p.rows == 32 ? go(tern_kv_attn_kernel<D, 2>, few(32), a, p, ws, st)
+                                      : go(tern_kv_attn_tile_kernel<D>, 2 * (D / 16) * 2 * 128 * 16, a, p, ws, st);
+  if (kernel_launched((int)e, p.rows <= 32 ? TERN_KERNEL_KV_ATTN : TERN_KERNEL_KV_ATTN_TILE)) return (int)e;
   if (!p.runs) return 0;
-  const int rows = std::min(p.rows, a.q_heads / a.cache.heads * a.batch.max_q);
-  tern_kv_attn_join_kernel<D><<<dim3(rows * a.cache.heads, a.batch.seqs * p.row_blocks), dim3(256), 0, st>>>(a, p, ws);
+  const int waves = std::min(p.rows, a.q_heads / a.cache.heads * a.batch.max_q) * a.cache.heads;
+  tern_kv_attn_join_kernel<D><<<dim3((waves + 3) / 4, a.batch.seqs * p.row_blocks), dim3(256), 0, st>>>(a, p, ws, waves);
   return kernel_launched((int)hipGetLastError(), TERN_KERNEL_KV_ATTN_JOIN);
 }
 

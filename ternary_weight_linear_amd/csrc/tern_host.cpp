@@ -54,8 +54,8 @@ const char* const kKernelNames[TERN_KERNEL_COUNT] = {
     "smallt_tile",     "smallt_tile_reduce", "b16_prefill",   "s8_mma",           "s8_reduce",
     "s8_row",          "s8_acc_export",     "stream_read",    "gemv_t5",          "chain",
     "smallt_narrow",   "rmsnorm",           "kv_append",      "kv_read",          "kv_attn",
-    "kv_attn_join"};
-static_assert(TERN_KERNEL_COUNT == 26, "one name per kernel id");
+    "kv_attn_tile",    "kv_attn_join"};
+static_assert(TERN_KERNEL_COUNT == 27, "one name per kernel id");
 
 // ------------------------------------------------------------ configuration
 

@@ -168,7 +168,7 @@ constexpr int kComputeUnits = 256;  // of the part that this library is built fo
 tern::KvAttnPlan plan_attn(const tern::KvAttnArgs& a) {
   tern::KvAttnPlan p{};
   const int64_t group = a.q_heads / a.cache.heads, rows = group * a.batch.max_q;
-  p.rows = rows <= 16 ? 16 : 32;
+  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
   p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
   const int64_t pages = attn_pages(a, std::min<int64_t>(a.batch.max_q, (p.rows + group - 2) / group + 1));
   const int64_t units = (int64_t)p.row_blocks * a.batch.seqs;
@@ -179,9 +179,14 @@ tern::KvAttnPlan plan_attn(const tern::KvAttnArgs& a) {
   // to 8192 tokens, 51 / 68 / 57 / 62 us for one of 131072; a workgroup a unit:
   // 71 us and 875 us); with two units each, 512 of equal lengths, runs and the
   // second kernel only cost (54 us, against 46 us without).
+  // The kernel for many rows is bound by its arithmetic and wants every
+  // workgroup that the registers admit: 2 a unit at 128 (219 us with 512 runs for
+  // a 1024-token chunk on 8192 keys, 290 with 256, 237 with 768, 282 without)
+  // and 1 at 256 (118 us for windowed chunks, 137 with 512, 135 without).
+  const int held = kComputeUnits * (p.rows <= 32 || a.cache.dim == 256 ? 1 : a.cache.dim == 128 ? 2 : 3);
   p.least = 8;
-  if (pages > p.least && units <= tern::kKvMaxUnits && units * a.cache.heads < 2 * kComputeUnits)
-    p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({kComputeUnits / a.cache.heads, units * pages / p.least, tern::kKvMaxRuns}));
+  if (pages > p.least && units <= tern::kKvMaxUnits && units * a.cache.heads < 2 * held)
+    p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({held / a.cache.heads, units * pages / p.least, tern::kKvMaxRuns}));
   return p;
 }
 
