@@ -72,6 +72,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, f16x2));
 }
 
+// Workgroup barrier that waits for this wave's LDS operations only, not for
+// the codes on their way from memory, as __syncthreads() would.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // vmcnt 63 (no wait), expcnt 7, lgkmcnt 0
+  asm volatile("s_barrier" ::: "memory");
+}
+
 // Maximum and sum over the four lanes that share lane & 15: the two halves
 // of the wave, then the two rows of 16 of each half, by register swaps.
 __device__ __forceinline__ float group_max(float v) {
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
         ids(base);  // codes of page i + 1 are already on their way
       }
       const int at = i - base;
-      __syncthreads();  // this page's operands are written, and the other buffer is read
+      lds_barrier();  // this page's operands are written, and the other buffer is read
       convert(tiles + (buffer ^ 1) * kPage);
       ask(at + 2);
       const u32x4* page = tiles + buffer * kPage + lane;
@@ -754,15 +761,15 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
   }
 }
 
-// Joins the runs of a unit, one wave a row: its lanes hold D / 64 elements
-// each and add the pieces in order.
+// Joins the runs of a unit: D / 4 lanes a row, four elements each, that add
+// the row's pieces in order, four pieces' loads at a time.
 template <int D>
-__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* ws, int waves) {
-  constexpr int E = D / 64, kMost = kKvMaxRuns / 64;
+__global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, KvAttnPlan plan, const float* ws, int count) {
+  constexpr int W = D / 4;
   const int heads = a.cache.heads, group = a.q_heads / heads;
-  const int lane = threadIdx.x & 63;
-  const int i = __builtin_amdgcn_readfirstlane((blockIdx.x * 256 + threadIdx.x) >> 6);  // (row, head) of the unit
-  if (i >= waves) return;
+  const int l = threadIdx.x % W;
+  const int i = blockIdx.x * (256 / W) + threadIdx.x / W;  // (row, head) of the unit
+  if (i >= count) return;
   const int head = i % heads, row = i / heads, u = blockIdx.y;
   const int* pre = (const int*)ws + 1;
   const int length = pre[-1], p0 = pre[u], p1 = pre[u + 1];
@@ -773,51 +780,36 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
   if (first == last) return;  // one piece: its workgroup wrote the result
   const int pieces = last - first + 1;  // 0: the row sees nothing
   const int64_t at = (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group;
-  // Piece i is in slot 0 of run first + i, but for the first one, in slot 1.
+  // Piece p is in slot 0 of run first + p, but for the first one, in slot 1.
   const int64_t slots = ((int64_t)head * plan.runs + first) * 2;
-  const float* po = ws + ws_head(a, plan) + (slots * plan.rows + row) * D + lane * E;
+  const float* po = ws + ws_head(a, plan) + (slots * plan.rows + row) * D + 4 * l;
   const float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * plan.rows * D + (slots * plan.rows + row) * 2;
-  float2 ml[kMost];
   float M = kNone;
+  for (int p = l; p < pieces; p += W) M = fmaxf(M, pm[(int64_t)(p ? 2 * p : 1) * plan.rows * 2]);
 #pragma unroll
-  for (int x = 0; x < kMost; ++x) {
-    const int p = lane + 64 * x;
-    ml[x] = p < pieces ? *(const float2*)(pm + (int64_t)(p ? 2 * p : 1) * plan.rows * 2) : float2{kNone, 0.f};
-    M = fmaxf(M, ml[x].x);
-  }
-  for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
+  for (int x = 1; x < W; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
   const float b = M == kNone ? 0.f : M;
   float L = 0.f;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int q = 0; q < pieces; q += 4) {
+    float2 ml[4];
+    f32x4 f[4];
 #pragma unroll
-  for (int x = 0; x < kMost; ++x) {
-    ml[x].x = __builtin_amdgcn_exp2f(ml[x].x - b);
-    L = __builtin_fmaf(ml[x].y, ml[x].x, L);
-  }
-  L = wave_sum(L);
-  float o[E] = {};
+    for (int j = 0; j < 4; ++j) {  // past the last piece, that one again with no weight
+      const int p = min(q + j, pieces - 1);
+      const int64_t slot = (int64_t)(p ? 2 * p : 1) * plan.rows;
+      ml[j] = *(const float2*)(pm + slot * 2);
+      f[j] = *(const f32x4*)(po + slot * D);
+    }
 #pragma unroll
-  for (int x = 0; x < kMost; ++x) {
-    const int most = min(pieces - 64 * x, 64);
-    for (int p0 = 0; p0 < most; p0 += 8) {  // eight loads at a time; past the last, that one again with no weight
-      float f[8][E];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int p = min(p0 + j, most - 1) + 64 * x;
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[j][e] = po[(int64_t)(p ? 2 * p : 1) * plan.rows * D + e];
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float y = p0 + j < most ? lane_float(ml[x].x, p0 + j) : 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(f[j][e], y, o[e]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float y = q + j < pieces ? __builtin_amdgcn_exp2f(ml[j].x - b) : 0.f;
+      L = __builtin_fmaf(ml[j].y, y, L);
+      o += f[j] * y;
     }
   }
   const float inv = L == 0.f ? 0.f : 1.0f / (L * kPScale);
-  uint16_t* out = a.out + at * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = (uint16_t)pack_bf16(o[e] * inv, 0.f);
+  *(uint2*)(a.out + at * D + 4 * l) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 template <class K>
@@ -840,8 +832,8 @@ int launch(const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) 
                                       : go(tern_kv_attn_tile_kernel<D>, 2 * (D / 16) * 2 * 128 * 16, a, p, ws, st);
   if (kernel_launched((int)e, p.rows <= 32 ? TERN_KERNEL_KV_ATTN : TERN_KERNEL_KV_ATTN_TILE)) return (int)e;
   if (!p.runs) return 0;
-  const int waves = std::min(p.rows, a.q_heads / a.cache.heads * a.batch.max_q) * a.cache.heads;
-  tern_kv_attn_join_kernel<D><<<dim3((waves + 3) / 4, a.batch.seqs * p.row_blocks), dim3(256), 0, st>>>(a, p, ws, waves);
+  const int count = std::min(p.rows, a.q_heads / a.cache.heads * a.batch.max_q) * a.cache.heads, each = 1024 / D;
+  tern_kv_attn_join_kernel<D><<<dim3((count + each - 1) / each, a.batch.seqs * p.row_blocks), dim3(256), 0, st>>>(a, p, ws, count);
   return kernel_launched((int)hipGetLastError(), TERN_KERNEL_KV_ATTN_JOIN);
 }
 
