@@ -481,10 +481,13 @@ typedef struct {
  *   kv_len [seqs]: tokens of the sequence, this call's among them;
  *   page_table [seqs][table_width]: page of its tokens 64 i .. 64 i + 63.
  * max_q and max_kv bound the rows and tokens of a sequence (they size the
- * launch); max_kv <= 64 table_width. The kernels check what they read: a
- * sequence whose arrays contradict these bounds, and a page outside the
- * cache, are left out (nothing is read or written for them; their attention
- * rows are those of a sequence without those keys).
+ * launch); max_kv <= 64 table_width. The kernels check what they read, so that
+ * no array can lead them outside the buffers: a sequence whose q_begin leaves
+ * the rows of the call or exceeds max_q is left out (its rows are not
+ * written); one whose kv_len is outside [0, max_kv], or (append and read)
+ * smaller than its rows of the call, appends and reads nothing and has no keys
+ * for the attention; a page outside the cache is not written, and its keys
+ * are absent.
  */
 typedef struct {
   const int32_t* q_begin;
@@ -546,7 +549,8 @@ tern_status tern_kv_read(const tern_kv_cache* cache, const tern_kv_batch* batch,
  * apart; out: bf16 [tokens][q_heads][dim]. q_heads a multiple of
  * cache->heads; scale > 0. The append of the call's tokens comes first.
  * ws: device, tern_kv_attn_workspace_bytes() bytes for the same arguments
- * (16-byte aligned; NULL if 0); calls that share it must not overlap.
+ * (16-byte aligned, any contents; NULL if 0); calls that share it must not
+ * overlap.
  * Scores and softmax statistics are fp32; probabilities enter the product with
  * the values as fp16 (11 bits). v scales below 2^-100 count as 2^-100.
  * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.

@@ -147,6 +147,8 @@ tern_status check_attn(const tern_kv_cache* cache, const tern_kv_batch* batch, i
   if (q_heads < cache->heads || q_heads % cache->heads != 0 || q_heads > 65535)
     return fail(TERN_ERR_SHAPE, "q_heads=%d must be a multiple of the cache's heads=%d, at most 65535", q_heads,
                 cache->heads);
+  if ((int64_t)(q_heads / cache->heads) * batch->max_q > (1 << 30))
+    return fail(TERN_ERR_SHAPE, "max_q=%d times %d query heads a kv head is too large", batch->max_q, q_heads / cache->heads);
   if (window < 0 || sinks < 0) return fail(TERN_ERR_VALUE, "window=%d and sinks=%d must not be negative", window, sinks);
   a->tokens = tokens, a->q_heads = q_heads;
   a->window = window >= batch->max_kv ? 0 : window;  // one that no sequence reaches hides nothing
@@ -185,7 +187,7 @@ tern::KvAttnPlan plan_attn(const tern::KvAttnArgs& a) {
   // and 1 at 256 (118 us for windowed chunks, 137 with 512, 135 without).
   const int held = kComputeUnits * (p.rows <= 32 || a.cache.dim == 256 ? 1 : a.cache.dim == 128 ? 2 : 3);
   p.least = 8;
-  if (pages > p.least && units <= tern::kKvMaxUnits && units * a.cache.heads < 2 * held)
+  if (pages > p.least && units <= tern::kKvMaxUnits && units * pages <= (1 << 30) && units * a.cache.heads < 2 * held)
     p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({held / a.cache.heads, units * pages / p.least, tern::kKvMaxRuns}));
   return p;
 }

@@ -130,3 +130,10 @@ def test_rope_table_and_sections(tl):
         tl.Rope.make(4, 8, sections=(3, 3))
     with pytest.raises(ValueError):
         tl.Rope.make(4, 8, sections=(9, -1))
+
+
+def test_attention_refuses_row_counts_past_32_bits(tl):
+    L = tl.lib()
+    c, b = structs(tl, dict(heads=1), dict(max_q=1 << 19))
+    assert L.tern_kv_attn_workspace_bytes(c, b, 3, 4096, 0, 0) == ctypes.c_size_t(-1).value
+    assert b"too large" in L.tern_last_error()
