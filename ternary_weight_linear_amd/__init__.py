@@ -294,7 +294,7 @@ def _current_stream() -> int:
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(_current_stream())
+        return _current_stream()
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -573,6 +573,14 @@ KV_PAGE = 64
 _KINDS = {}  # dtype -> tern_dtype
 
 
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream` (see _on)."""
+    if stream is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        return _torch().empty(shape, dtype=dtype, device=device)
+
+
 def _rows(t, name, shape, device):
     """Checks a device matrix (or a matrix of heads) whose rows may lie apart:
     float32 or bfloat16, its shape and device, each row contiguous. Returns
@@ -613,27 +621,30 @@ def _on_gpu(t, name):
 def _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream, made=False):
     """`made`: q, scale and y are this module's own, of the right shape."""
     device = _on_gpu(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
-    T, K = x.shape
-    xt, xs = _rows(x, "x", (T, K), device)
-    wt, _ = _rows(weight if weight.dim() == 2 else weight[None], "weight", (1, K), device)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, K], got {tuple(shape)}")
+    T, K = shape
+    xt, xs = _rows(x, "x", shape, device)
+    wt, _ = _rows(weight, "weight", shape[1:], device)
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
     rp = op = qp = sp = yp = None
     rt = rs = os_ = ys = 0
     if residual is not None:
-        rt, rs = _rows(residual, "residual", (T, K), device)
+        rt, rs = _rows(residual, "residual", shape, device)
         rp = residual.data_ptr()
         if residual_out is None or residual_out is residual:
             op, os_ = rp, rs
         else:
-            ot, os_ = _rows(residual_out, "residual_out", (T, K), device)
+            ot, os_ = _rows(residual_out, "residual_out", shape, device)
             if ot != rt:
                 raise TypeError("residual_out must have the residual's type")
             op = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     if y is not None:
-        yt, ys = (1, K) if made else _rows(y, "y", (T, K), device)
+        yt, ys = (1, K) if made else _rows(y, "y", shape, device)
         if yt != 1:
             raise TypeError(f"y must be bfloat16, got {y.dtype}")
         yp = y.data_ptr()
@@ -652,9 +663,7 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, strea
     residual_out (default: the residual itself) in the residual's type."""
     made = y is None
     if made:
-        torch = _torch()
-        with _on(stream):
-            y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        y = _empty(x.shape, _torch().bfloat16, x.device, stream)
     _norm(x, weight, eps, residual, residual_out, None, None, "row_major", y, stream, made)
     return y
 
@@ -664,13 +673,10 @@ def rmsnorm_s8(x, weight, eps=1e-6, residual=None, residual_out=None, q=None, sc
     """rmsnorm with an 8-bit output: (q int8 [T, K] in `layout`, scale float32
     [T]), as linear_s8_q takes them; `y` (bf16) is written too when given."""
     made = q is None and scale is None and y is None
-    if q is None or scale is None:
-        torch = _torch()
-        with _on(stream):
-            if q is None:
-                q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-            if scale is None:
-                scale = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    if q is None:
+        q = _empty(x.shape, _torch().int8, x.device, stream)
+    if scale is None:
+        scale = _empty(x.shape[:1], _torch().float32, x.device, stream)
     _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream, made)
     return q, scale
 
@@ -792,9 +798,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Ro
         shape = (tokens, heads, d)
         qt, qs = _rows(q, "q", shape, device)
         if q_out is None:
-            torch = _torch()
-            with _on(stream):
-                q_out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+            q_out = _empty(shape, _torch().bfloat16, device, stream)
         else:
             _dev(q_out, _torch().bfloat16, "q_out", shape, device)
         qp, op = q.data_ptr(), q_out.data_ptr()
@@ -825,15 +829,14 @@ def kv_read(cache: KVCache, batch: KVBatch, rows: int, k_out=None, v_out=None, s
     q_begin[s + 1] - q_begin[s] tokens."""
     bf16 = _torch().bfloat16
     shape = (rows, cache.heads, cache.d)
-    with _on(stream):
-        if k_out is None:
-            k_out = _torch().empty(shape, dtype=bf16, device=cache.device)
-        else:
-            _dev(k_out, bf16, "k_out", shape, cache.device)
-        if v_out is None:
-            v_out = _torch().empty(shape, dtype=bf16, device=cache.device)
-        else:
-            _dev(v_out, bf16, "v_out", shape, cache.device)
+    if k_out is None:
+        k_out = _empty(shape, bf16, cache.device, stream)
+    else:
+        _dev(k_out, bf16, "k_out", shape, cache.device)
+    if v_out is None:
+        v_out = _empty(shape, bf16, cache.device, stream)
+    else:
+        _dev(v_out, bf16, "v_out", shape, cache.device)
     _same_device(batch, cache)
     _check(lib().tern_kv_read(cache._ref, batch._ref, rows, k_out.data_ptr(), v_out.data_ptr(), _stream(stream)))
     return k_out, v_out
@@ -873,8 +876,7 @@ def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, si
         raise TypeError(f"q must be bfloat16, got {q.dtype}")
     _same_device(batch, cache)
     if out is None:
-        with _on(stream):
-            out = _torch().empty(shape, dtype=q.dtype, device=device)
+        out = _empty(shape, q.dtype, device, stream)
     else:
         _dev(out, q.dtype, "out", shape, device)
     if workspace is None:
