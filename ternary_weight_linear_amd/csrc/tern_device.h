@@ -5,8 +5,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 namespace tern {
 namespace dev {
 
@@ -152,90 +150,6 @@ __device__ __forceinline__ void limb_chunk(const u32x4& lo, const u32x4& hi, int
     limb_chunk_t<true>(lo, hi, __builtin_ldexpf(1.0f, -d - 64), o0, o1, o2);
   else
     limb_chunk_t<false>(lo, hi, __builtin_ldexpf(1.0f, -d), o0, o1, o2);
-}
-
-// ---- int8 codes of activations and cache values: clamp(rne(v / scale)).
-
-__device__ __forceinline__ uint32_t quant_code(float v, float sc) {
-  const float r = rintf(v / sc);  // IEEE division, ties-to-even rounding
-  const float c = fminf(fmaxf(r, -127.f), 127.f);
-  return (uint32_t)((int)c) & 0xffu;
-}
-__device__ __forceinline__ uint32_t quant_byte(uint32_t xbits, float sc) {
-  return quant_code(__uint_as_float(xbits), sc);
-}
-
-// The same code from y = fl(v * r), r = fl(1 / sc), sc a normal float: with
-// |v| <= 127 sc, y is within 2^-16 of v / sc and the IEEE quotient within
-// 2^-17, so unless y lies within 2^-15 of a half-integer both round to the
-// same integer. Such values set `near`, and the caller redoes them with the
-// division.
-__device__ __forceinline__ uint32_t quant_code_rcp(float v, float r, bool& near) {
-#pragma clang fp contract(off)
-  const float y = v * r;
-  const float t = rintf(y);
-  near |= !(fabsf(y - t) < 0.5f - 0x1p-15f);
-  const float c = fminf(fmaxf(t, -127.f), 127.f);
-  return (uint32_t)((int)c) & 0xffu;
-}
-
-// Codes of 16 values (4 dwords, byte e of dword d = value 4d + e): by the
-// reciprocal when the token's scale allows it and no value is near a rounding
-// boundary, else by division.
-__device__ __forceinline__ void quant_codes16(const float (&v)[16], float sc, float r, bool rcp_ok,
-                                              uint32_t (&w)[4]) {
-  bool near = !rcp_ok;
-  if (rcp_ok) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-      w[d] = quant_code_rcp(v[4 * d], r, near) | (quant_code_rcp(v[4 * d + 1], r, near) << 8) |
-             (quant_code_rcp(v[4 * d + 2], r, near) << 16) | (quant_code_rcp(v[4 * d + 3], r, near) << 24);
-  }
-  if (near) {
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-      w[d] = quant_code(v[4 * d], sc) | (quant_code(v[4 * d + 1], sc) << 8) |
-             (quant_code(v[4 * d + 2], sc) << 16) | (quant_code(v[4 * d + 3], sc) << 24);
-  }
-}
-
-// The s8 kernel's operand order inside every 64-byte k-block kb: byte
-// 16g + 4i + beta holds k = 64kb + 8g + kmap(i, beta) with
-// kmap(i, .) = {32 + 2i, 2i, 33 + 2i, 2i + 1}. It is the order in which
-// (word << 2i) & 0xC0C0C0C0 lays out the codes of a packed weight word (see
-// weights_operand_i8), so activations stored this way feed the MFMA as is.
-// From the natural order (lo = bytes 8g..8g+7, hi = bytes 32+8g..32+8g+7 of
-// the block) each dword is one byte permute.
-__device__ __forceinline__ u32x4 s8_operand_order(uint32_t L0, uint32_t L1, uint32_t H0,
-                                                  uint32_t H1) {
-  return u32x4{__builtin_amdgcn_perm(H0, L0, 0x01050004u), __builtin_amdgcn_perm(H0, L0, 0x03070206u),
-               __builtin_amdgcn_perm(H1, L1, 0x01050004u), __builtin_amdgcn_perm(H1, L1, 0x03070206u)};
-}
-
-// ---- bf16 conversions and reductions of the decoder operators (norm, cache).
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// Two floats rounded to nearest even bf16, packed (NaN stays NaN).
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 v = {(__bf16)lo, (__bf16)hi};
-  return __builtin_bit_cast(uint32_t, v);
-}
-
-// Sum over the 64 lanes, the same in every lane and in a fixed order: a
-// butterfly inside each row of 16 lanes (every lane of a pair adds the same
-// two numbers), then the four row sums.
-__device__ __forceinline__ float wave_sum(float v) {
-  auto dpp = [](float x, auto ctrl) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
-  };
-  v += dpp(v, std::integral_constant<int, 0xb1>{});   // quad_perm [1,0,3,2]
-  v += dpp(v, std::integral_constant<int, 0x4e>{});   // quad_perm [2,3,0,1]
-  v += dpp(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
-  v += dpp(v, std::integral_constant<int, 0x140>{});  // row_mirror
-  auto lane = [&](int i) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), i)); };
-  return (lane(0) + lane(16)) + (lane(32) + lane(48));
 }
 }  // namespace dev
 }  // namespace tern

@@ -16,6 +16,62 @@ using namespace dev;
 // per-token int8 activation quantisation
 // --------------------------------------------------------------------------
 
+__device__ __forceinline__ uint32_t quant_code(float v, float sc) {
+  const float r = rintf(v / sc);  // IEEE division, ties-to-even rounding
+  const float c = fminf(fmaxf(r, -127.f), 127.f);
+  return (uint32_t)((int)c) & 0xffu;
+}
+__device__ __forceinline__ uint32_t quant_byte(uint32_t xbits, float sc) {
+  return quant_code(__uint_as_float(xbits), sc);
+}
+
+// The same code from y = fl(v * r), r = fl(1 / sc), sc a normal float: with
+// |v| <= 127 sc, y is within 2^-16 of v / sc and the IEEE quotient within
+// 2^-17, so unless y lies within 2^-15 of a half-integer both round to the
+// same integer. Such values set `near`, and the caller redoes them with the
+// division.
+__device__ __forceinline__ uint32_t quant_code_rcp(float v, float r, bool& near) {
+#pragma clang fp contract(off)
+  const float y = v * r;
+  const float t = rintf(y);
+  near |= !(fabsf(y - t) < 0.5f - 0x1p-15f);
+  const float c = fminf(fmaxf(t, -127.f), 127.f);
+  return (uint32_t)((int)c) & 0xffu;
+}
+
+// Codes of 16 values (4 dwords, byte e of dword d = value 4d + e): by the
+// reciprocal when the token's scale allows it and no value is near a rounding
+// boundary, else by division.
+__device__ __forceinline__ void quant_codes16(const float (&v)[16], float sc, float r, bool rcp_ok,
+                                              uint32_t (&w)[4]) {
+  bool near = !rcp_ok;
+  if (rcp_ok) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      w[d] = quant_code_rcp(v[4 * d], r, near) | (quant_code_rcp(v[4 * d + 1], r, near) << 8) |
+             (quant_code_rcp(v[4 * d + 2], r, near) << 16) | (quant_code_rcp(v[4 * d + 3], r, near) << 24);
+  }
+  if (near) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      w[d] = quant_code(v[4 * d], sc) | (quant_code(v[4 * d + 1], sc) << 8) |
+             (quant_code(v[4 * d + 2], sc) << 16) | (quant_code(v[4 * d + 3], sc) << 24);
+  }
+}
+
+// The s8 kernel's operand order inside every 64-byte k-block kb: byte
+// 16g + 4i + beta holds k = 64kb + 8g + kmap(i, beta) with
+// kmap(i, .) = {32 + 2i, 2i, 33 + 2i, 2i + 1}. It is the order in which
+// (word << 2i) & 0xC0C0C0C0 lays out the codes of a packed weight word (see
+// weights_operand_i8), so activations stored this way feed the MFMA as is.
+// From the natural order (lo = bytes 8g..8g+7, hi = bytes 32+8g..32+8g+7 of
+// the block) each dword is one byte permute.
+__device__ __forceinline__ u32x4 s8_operand_order(uint32_t L0, uint32_t L1, uint32_t H0,
+                                                  uint32_t H1) {
+  return u32x4{__builtin_amdgcn_perm(H0, L0, 0x01050004u), __builtin_amdgcn_perm(H0, L0, 0x03070206u),
+               __builtin_amdgcn_perm(H1, L1, 0x01050004u), __builtin_amdgcn_perm(H1, L1, 0x03070206u)};
+}
+
 // Per-token quantisation. One block per token: absmax (DPP wave reduction,
 // then across the 4 waves), scale = absmax / 127, then the codes. PERM writes
 // them in the s8 operand order (K % 64 == 0), otherwise row-major.
