@@ -215,7 +215,8 @@ struct Queries {
   int pos[NT];         // the row's position
 
   // Asks for the rows from `row` of a sequence on; rows past its last repeat that.
-  __device__ __forceinline__ void ask(const KvAttnArgs& a, const Seq& seq, int row, int rows, int head, int group, int n, int g) {
+  __device__ __forceinline__ void ask(const KvAttnArgs& a, const Seq& seq, int row, int rows, int head, int group,
+                                      int n, int g) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int rr = min(row + 16 * t + n, rows - 1);
@@ -328,7 +329,8 @@ __device__ __forceinline__ void write_row(const KvAttnArgs& a, const f32x4 (&o)[
     *(uint2*)(out + 16 * h) = uint2{pack_bf16(o[h][0] * inv, o[h][1] * inv), pack_bf16(o[h][2] * inv, o[h][3] * inv)};
 }
 template <int D>
-__device__ __forceinline__ void write_part(float* po, float* pm, const f32x4 (&o)[D / 16], float M, float L, int row, int g) {
+__device__ __forceinline__ void write_part(float* po, float* pm, const f32x4 (&o)[D / 16], float M, float L, int row,
+                                           int g) {
 #pragma unroll
   for (int h = 0; h < D / 16; ++h) *(f32x4*)(po + row * D + 16 * h + 4 * g) = o[h];
   if (g == 0) *(float2*)(pm + row * 2) = float2{M, L};
@@ -365,212 +367,212 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
     if (run.begin >= run.end) return;
   }
   for (int u = run.unit, from = run.begin;;) {
-  const Unit unit = unit_of(a, plan, u);
-  if (unit.rlast < unit.r0) return;  // only without runs: no pages, no run here
-  const Seq seq = unit.seq;
-  const Pages pages = unit.pages;
-  const int r0 = unit.r0, rows = unit.rows, rlast = unit.rlast;
-  const int begin = plan.runs ? __builtin_amdgcn_readfirstlane(from - pre[u]) : 0;
-  const int end = plan.runs ? min(pages.count, begin + run.end - from) : pages.count;
+    const Unit unit = unit_of(a, plan, u);
+    if (unit.rlast < unit.r0) return;  // only without runs: no pages, no run here
+    const Seq seq = unit.seq;
+    const Pages pages = unit.pages;
+    const int r0 = unit.r0, rows = unit.rows, rlast = unit.rlast;
+    const int begin = plan.runs ? __builtin_amdgcn_readfirstlane(from - pre[u]) : 0;
+    const int end = plan.runs ? min(pages.count, begin + run.end - from) : pages.count;
 
-  // Page ids and scales of this wave's next 64 pages, one a lane; then keys
-  // and values, asked for one buffer ahead of their use: a page's 16-byte
-  // loads (N of keys, N of values a lane) go through two buffers of B in turn,
-  // and each buffer is refilled as soon as it has been used. Streamed once:
-  // non-temporal.
-  constexpr int N = D / 16, B = N < 8 ? N : 8, H = N / B;
-  u32x4 buf[2][B];
-  const int32_t* table = a.batch.page_table + (int64_t)(u / plan.row_blocks) * a.batch.table_width;
-  int id = -1, steps = 0;
-  float ks = 0.f, vs = 0.f;
-  auto ids = [&](int base) {
-    const int mine = base + wave + 4 * lane;
-    steps = (min(end, base + 256) - base - wave + 3) >> 2;
-    id = mine < end ? table[pages.at(mine)] : -1;
-  };
-  auto scales = [&]() {
-    if (id >= a.cache.pages) id = -1;
-    ks = vs = 0.f;
-    if (id >= 0) {
-      const int64_t ph = (int64_t)id * heads + head;
-      ks = a.cache.k_scale[ph];
-      vs = a.cache.v_scale[ph];
-    }
-  };
-  // Part h (0..2H-1: keys, then values) of step i's page into its buffer. A
-  // page outside the cache, and one past the last step, are buffers of no
-  // bytes: they read as zeros and cost no traffic, and every step issues the
-  // same loads, so that a wait for one of them never waits for a later one.
-  auto ask = [&](int i, int h) {
-    const int pid = i < steps ? __builtin_amdgcn_readlane(id, i) : -1;
-    const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
-    const rsrc_t page = make_rsrc((h < H ? a.cache.k : a.cache.v) + off, pid < 0 ? 0 : kKvPage * D);
-    const int lane_at = h < H ? n * D + 16 * g : n * kKvPage + 16 * g;
-#pragma unroll
-    for (int j = 0; j < B; ++j) {
-      const int x = h % H * B + j;  // keys: tokens 16 (x / C) .., elements 64 (x % C) ..; values: elements 16 x ..
-      const int at = h < H ? 16 * (x / C) * D + 64 * (x % C) : 16 * x * kKvPage;
-      buf[h & 1][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(page, lane_at, at, kAuxNontemporal));
-    }
-  };
-  auto start = [&]() {
-    scales();
-    ask(0, 0);
-    ask(0, 1);
-  };
-  // The chain of dependent loads at the start (lengths, page ids, scales and
-  // codes) is what a short call waits for: everything is asked for as soon as
-  // its address is known, the query rows between the ids and the codes.
-  ids(begin);
-  Queries<D, NT> q;
-  q.ask(a, seq, r0, rows, head, group, n, g);
-  __builtin_amdgcn_sched_barrier(0);
-  start();
-  __builtin_amdgcn_sched_barrier(0);
-  q.make(a.scale);
-  const int pos_min = seq.kv - seq.n + r0 / group, pos_max = seq.kv - seq.n + rlast / group;
-
-  f32x4 o[NT][HT];
-  float M[NT], L[NT];  // L: this lane's share of the sum
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    M[t] = kNone;
-    L[t] = 0.f;
-#pragma unroll
-    for (int i = 0; i < HT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-
-  for (int base = begin; base < end;) {
-    vs = vs < kLeastScale ? kLeastScale : vs;
-    const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / (vs * kPScale);
-    for (int i = 0; i < steps; ++i) {
-      // What follows part h in its buffer: part h + 2 of this page or the next one's.
-      auto refill = [&](int h) {
-        if (h + 2 < 2 * H)
-          ask(i, h + 2);
-        else
-          ask(i + 1, h + 2 - 2 * H);
-      };
-      const PageScales w{lane_float(ks, i), lane_float(lv, i), lane_float(iv, i), __builtin_amdgcn_readlane(id, i) < 0};
-      const int j0 = pages.at(base + wave + 4 * i) * kKvPage;
-
-      f32x4 s[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) s[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          const int x = h * B + j, b = x / C, c = x % C;
-          const u32x4 x16 = buf[h & 1][j];
-          const f16x8 k0 = codes8(x16[0], x16[1]), k1 = codes8(x16[2], x16[3]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q.op[t][c][0], s[t][b], 0, 0, 0);
-            s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q.op[t][c][1], s[t][b], 0, 0, 0);
-          }
-        }
-        refill(h);
+    // Page ids and scales of this wave's next 64 pages, one a lane; then keys
+    // and values, asked for one buffer ahead of their use: a page's 16-byte
+    // loads (N of keys, N of values a lane) go through two buffers of B in turn,
+    // and each buffer is refilled as soon as it has been used. Streamed once:
+    // non-temporal.
+    constexpr int N = D / 16, B = N < 8 ? N : 8, H = N / B;
+    u32x4 buf[2][B];
+    const int32_t* table = a.batch.page_table + (int64_t)(u / plan.row_blocks) * a.batch.table_width;
+    int id = -1, steps = 0;
+    float ks = 0.f, vs = 0.f;
+    auto ids = [&](int base) {
+      const int mine = base + wave + 4 * lane;
+      steps = (min(end, base + 256) - base - wave + 3) >> 2;
+      id = mine < end ? table[pages.at(mine)] : -1;
+    };
+    auto scales = [&]() {
+      if (id >= a.cache.pages) id = -1;
+      ks = vs = 0.f;
+      if (id >= 0) {
+        const int64_t ph = (int64_t)id * heads + head;
+        ks = a.cache.k_scale[ph];
+        vs = a.cache.v_scale[ph];
       }
+    };
+    // Part h (0..2H-1: keys, then values) of step i's page into its buffer. A
+    // page outside the cache, and one past the last step, are buffers of no
+    // bytes: they read as zeros and cost no traffic, and every step issues the
+    // same loads, so that a wait for one of them never waits for a later one.
+    auto ask = [&](int i, int h) {
+      const int pid = i < steps ? __builtin_amdgcn_readlane(id, i) : -1;
+      const int64_t off = ((int64_t)pid * heads + head) * (kKvPage * D);
+      const rsrc_t page = make_rsrc((h < H ? a.cache.k : a.cache.v) + off, pid < 0 ? 0 : kKvPage * D);
+      const int lane_at = h < H ? n * D + 16 * g : n * kKvPage + 16 * g;
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        const int x = h % H * B + j;  // keys: tokens 16 (x / C) .., elements 64 (x % C) ..; values: elements 16 x ..
+        const int at = h < H ? 16 * (x / C) * D + 64 * (x % C) : 16 * x * kKvPage;
+        buf[h & 1][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(page, lane_at, at, kAuxNontemporal));
+      }
+    };
+    auto start = [&]() {
+      scales();
+      ask(0, 0);
+      ask(0, 1);
+    };
+    // The chain of dependent loads at the start (lengths, page ids, scales and
+    // codes) is what a short call waits for: everything is asked for as soon as
+    // its address is known, the query rows between the ids and the codes.
+    ids(begin);
+    Queries<D, NT> q;
+    q.ask(a, seq, r0, rows, head, group, n, g);
+    __builtin_amdgcn_sched_barrier(0);
+    start();
+    __builtin_amdgcn_sched_barrier(0);
+    q.make(a.scale);
+    const int pos_min = seq.kv - seq.n + r0 / group, pos_max = seq.kv - seq.n + rlast / group;
 
-      // Whether every row sees the whole page.
-      const bool whole = !w.absent && j0 + kKvPage - 1 <= pos_min &&
-                         (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
-      f16x8 pf[NT][2];
-      float alpha[NT];
-      auto softmax = [&](auto masked) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          page_softmax<decltype(masked)::value>(s[t], w, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
-                                                alpha[t], pf[t]);
-      };
-      if (whole)
-        softmax(std::false_type{});
-      else
-        softmax(std::true_type{});
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (__any(alpha[t] != 1.f)) {  // a maximum moved (or a row is NaN)
-#pragma unroll
-          for (int x = 0; x < HT; ++x) o[t][x] *= alpha[t];
-        }
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-#pragma unroll
-        for (int j = 0; j < B; ++j) {
-          const int x = h * B + j;
-          const u32x4 x16 = buf[(H + h) & 1][j];
-          const f16x8 v0 = codes8(x16[0], x16[1]), v1 = codes8(x16[2], x16[3]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][x], 0, 0, 0);
-            o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][x], 0, 0, 0);
-          }
-        }
-        refill(H + h);
-      }
-    }
-    base += 256;
-    if (base < end) {
-      ids(base);
-      start();
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) L[t] = group_sum(L[t]);
-
-  // Join the four waves: 2 and 3 into 0 and 1, then 1 into 0.
-#pragma unroll
-  for (int half = 2; half >= 1; half >>= 1) {
-    float* slot = lds + wave % half * kSlot;
-    float* ml = slot + R * D;
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int h = 0; h < HT; ++h) *(f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) = o[t][h];
-        if (g == 0) ml[16 * t + n] = M[t], ml[R + 16 * t + n] = L[t];
-      }
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const float m2 = ml[16 * t + n], l2 = ml[R + 16 * t + n];
-        const float Mn = fmaxf(M[t], m2), b = Mn == kNone ? 0.f : Mn;
-        const float x = __builtin_amdgcn_exp2f(M[t] - b), y = __builtin_amdgcn_exp2f(m2 - b);
-        M[t] = Mn;
-        L[t] = L[t] * x + l2 * y;
-#pragma unroll
-        for (int h = 0; h < HT; ++h)
-          o[t][h] = o[t][h] * x + *(const f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) * y;
-      }
-    }
-    __syncthreads();
-  }
-  if (wave == 0) {
-    const bool whole = begin == 0 && end == pages.count;
-    const int64_t slot = ((int64_t)head * plan.runs + w) * 2 + (begin == 0);
-    float* po = ws + ws_head(a, plan) + slot * R * D;
-    float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * R * D + slot * R * 2;
+    f32x4 o[NT][HT];
+    float M[NT], L[NT];  // L: this lane's share of the sum
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = r0 + 16 * t + n;
-      if (r >= rows) continue;
-      if (whole)
-        write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g);
-      else
-        write_part<D>(po, pm, o[t], M[t], L[t], 16 * t + n, g);
+      M[t] = kNone;
+      L[t] = 0.f;
+#pragma unroll
+      for (int i = 0; i < HT; ++i) o[t][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-  }
-  if (!plan.runs) return;
-  from += end - begin;
-  if (from >= run.end) return;
-  do ++u;
-  while (pre[u + 1] == pre[u]);  // the next unit with pages: there is one before run.end
-  u = __builtin_amdgcn_readfirstlane(u);
+
+    for (int base = begin; base < end;) {
+      vs = vs < kLeastScale ? kLeastScale : vs;
+      const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / (vs * kPScale);
+      for (int i = 0; i < steps; ++i) {
+        // What follows part h in its buffer: part h + 2 of this page or the next one's.
+        auto refill = [&](int h) {
+          if (h + 2 < 2 * H)
+            ask(i, h + 2);
+          else
+            ask(i + 1, h + 2 - 2 * H);
+        };
+        const PageScales w{lane_float(ks, i), lane_float(lv, i), lane_float(iv, i), __builtin_amdgcn_readlane(id, i) < 0};
+        const int j0 = pages.at(base + wave + 4 * i) * kKvPage;
+
+        f32x4 s[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) s[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            const int x = h * B + j, b = x / C, c = x % C;
+            const u32x4 x16 = buf[h & 1][j];
+            const f16x8 k0 = codes8(x16[0], x16[1]), k1 = codes8(x16[2], x16[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, q.op[t][c][0], s[t][b], 0, 0, 0);
+              s[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k1, q.op[t][c][1], s[t][b], 0, 0, 0);
+            }
+          }
+          refill(h);
+        }
+
+        // Whether every row sees the whole page.
+        const bool whole = !w.absent && j0 + kKvPage - 1 <= pos_min &&
+                           (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
+        f16x8 pf[NT][2];
+        float alpha[NT];
+        auto softmax = [&](auto masked) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            page_softmax<decltype(masked)::value>(s[t], w, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
+                                                  alpha[t], pf[t]);
+        };
+        if (whole)
+          softmax(std::false_type{});
+        else
+          softmax(std::true_type{});
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          if (__any(alpha[t] != 1.f)) {  // a maximum moved (or a row is NaN)
+#pragma unroll
+            for (int x = 0; x < HT; ++x) o[t][x] *= alpha[t];
+          }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+#pragma unroll
+          for (int j = 0; j < B; ++j) {
+            const int x = h * B + j;
+            const u32x4 x16 = buf[(H + h) & 1][j];
+            const f16x8 v0 = codes8(x16[0], x16[1]), v1 = codes8(x16[2], x16[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][x], 0, 0, 0);
+              o[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][x], 0, 0, 0);
+            }
+          }
+          refill(H + h);
+        }
+      }
+      base += 256;
+      if (base < end) {
+        ids(base);
+        start();
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) L[t] = group_sum(L[t]);
+
+    // Join the four waves: 2 and 3 into 0 and 1, then 1 into 0.
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+      float* slot = lds + wave % half * kSlot;
+      float* ml = slot + R * D;
+      if (wave >= half && wave < 2 * half) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int h = 0; h < HT; ++h) *(f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) = o[t][h];
+          if (g == 0) ml[16 * t + n] = M[t], ml[R + 16 * t + n] = L[t];
+        }
+      }
+      __syncthreads();
+      if (wave < half) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const float m2 = ml[16 * t + n], l2 = ml[R + 16 * t + n];
+          const float Mn = fmaxf(M[t], m2), b = Mn == kNone ? 0.f : Mn;
+          const float x = __builtin_amdgcn_exp2f(M[t] - b), y = __builtin_amdgcn_exp2f(m2 - b);
+          M[t] = Mn;
+          L[t] = L[t] * x + l2 * y;
+#pragma unroll
+          for (int h = 0; h < HT; ++h)
+            o[t][h] = o[t][h] * x + *(const f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) * y;
+        }
+      }
+      __syncthreads();
+    }
+    if (wave == 0) {
+      const bool whole = begin == 0 && end == pages.count;
+      const int64_t slot = ((int64_t)head * plan.runs + w) * 2 + (begin == 0);
+      float* po = ws + ws_head(a, plan) + slot * R * D;
+      float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * R * D + slot * R * 2;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int r = r0 + 16 * t + n;
+        if (r >= rows) continue;
+        if (whole)
+          write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g);
+        else
+          write_part<D>(po, pm, o[t], M[t], L[t], 16 * t + n, g);
+      }
+    }
+    if (!plan.runs) return;
+    from += end - begin;
+    if (from >= run.end) return;
+    do ++u;
+    while (pre[u + 1] == pre[u]);  // the next unit with pages: there is one before run.end
+    u = __builtin_amdgcn_readfirstlane(u);
   }
 }
 
@@ -646,8 +648,10 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
 #pragma unroll
       for (int j = 0; j < N / 4; ++j) {
         const int x = wave + 4 * j;
-        raw[0][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, n * D + 16 * g, 16 * (x / C) * D + 64 * (x % C), 0));
-        raw[1][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, n * kKvPage + 16 * g, 16 * x * kKvPage, 0));
+        raw[0][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  kr, n * D + 16 * g, 16 * (x / C) * D + 64 * (x % C), 0));
+        raw[1][j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                  vr, n * kKvPage + 16 * g, 16 * x * kKvPage, 0));
       }
     };
     auto convert = [&](u32x4* to) {
@@ -850,7 +854,8 @@ int launch(const KvAttnArgs& a, const KvAttnPlan& p, float* ws, hipStream_t st) 
   if (kernel_launched((int)e, p.rows <= 32 ? TERN_KERNEL_KV_ATTN : TERN_KERNEL_KV_ATTN_TILE)) return (int)e;
   if (!p.runs) return 0;
   const int count = std::min(p.rows, a.q_heads / a.cache.heads * a.batch.max_q) * a.cache.heads, each = 1024 / D;
-  tern_kv_attn_join_kernel<D><<<dim3((count + each - 1) / each, a.batch.seqs * p.row_blocks), dim3(256), 0, st>>>(a, p, ws, count);
+  const dim3 grid((count + each - 1) / each, a.batch.seqs * p.row_blocks);
+  tern_kv_attn_join_kernel<D><<<grid, dim3(256), 0, st>>>(a, p, ws, count);
   return kernel_launched((int)hipGetLastError(), TERN_KERNEL_KV_ATTN_JOIN);
 }
 

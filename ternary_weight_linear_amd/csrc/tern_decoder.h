@@ -36,11 +36,13 @@ struct Coder {
     bool near = false;
 #pragma unroll
     for (int d = 0; d < 4; ++d)
-      w[d] = quick(v[4 * d], near) | quick(v[4 * d + 1], near) << 8 | quick(v[4 * d + 2], near) << 16 | quick(v[4 * d + 3], near) << 24;
+      w[d] = quick(v[4 * d], near) | quick(v[4 * d + 1], near) << 8 | quick(v[4 * d + 2], near) << 16 |
+             quick(v[4 * d + 3], near) << 24;
     if (near) {
 #pragma unroll
       for (int d = 0; d < 4; ++d)
-        w[d] = divided(v[4 * d]) | divided(v[4 * d + 1]) << 8 | divided(v[4 * d + 2]) << 16 | divided(v[4 * d + 3]) << 24;
+        w[d] = divided(v[4 * d]) | divided(v[4 * d + 1]) << 8 | divided(v[4 * d + 2]) << 16 |
+               divided(v[4 * d + 3]) << 24;
     }
   }
 };
@@ -68,7 +70,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // two numbers), then the four row sums.
 __device__ __forceinline__ float wave_sum(float v) {
   auto dpp = [](float x, auto ctrl) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, false));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), decltype(ctrl)::value, 0xf,
+                                                                 0xf, false));
   };
   v += dpp(v, std::integral_constant<int, 0xb1>{});   // quad_perm [1,0,3,2]
   v += dpp(v, std::integral_constant<int, 0x4e>{});   // quad_perm [2,3,0,1]

@@ -148,7 +148,8 @@ tern_status check_attn(const tern_kv_cache* cache, const tern_kv_batch* batch, i
     return fail(TERN_ERR_SHAPE, "q_heads=%d must be a multiple of the cache's heads=%d, at most 65535", q_heads,
                 cache->heads);
   if ((int64_t)(q_heads / cache->heads) * batch->max_q > (1 << 30))
-    return fail(TERN_ERR_SHAPE, "max_q=%d times %d query heads a kv head is too large", batch->max_q, q_heads / cache->heads);
+    return fail(TERN_ERR_SHAPE, "max_q=%d times %d query heads a kv head is too large", batch->max_q,
+                q_heads / cache->heads);
   if (window < 0 || sinks < 0) return fail(TERN_ERR_VALUE, "window=%d and sinks=%d must not be negative", window, sinks);
   a->tokens = tokens, a->q_heads = q_heads;
   a->window = window >= batch->max_kv ? 0 : window;  // one that no sequence reaches hides nothing
@@ -216,7 +217,8 @@ tern_status tern_kv_attn(const tern_kv_cache* cache, const tern_kv_batch* batch,
   tern::KvAttnArgs a{};
   if (tern_status st = check_attn(cache, batch, tokens, q_heads, window, sinks, &a)) return st;
   if (!q_bf16 || !out_bf16) return fail(TERN_ERR_NULL, "tern_kv_attn: q or out is NULL");
-  if (!(scale > 0.f) || std::isinf(scale)) return fail(TERN_ERR_VALUE, "scale=%g must be finite and positive", (double)scale);
+  if (!(scale > 0.f) || std::isinf(scale))
+    return fail(TERN_ERR_VALUE, "scale=%g must be finite and positive", (double)scale);
   if (q_stride < (int64_t)q_heads * cache->dim) return fail(TERN_ERR_SHAPE, "q_stride is smaller than a row");
   if (!aligned16(q_bf16) || !aligned16(out_bf16) || q_stride % 8 != 0)
     return fail(TERN_ERR_ALIGN, "tern_kv_attn: q, its rows and out must be 16-byte aligned");

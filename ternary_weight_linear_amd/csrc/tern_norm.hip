@@ -154,14 +154,24 @@ void go(const NormArgs& a, hipStream_t st) {
     tern_rmsnorm_kernel<XT, RT, 2><<<dim3(a.T), dim3(nt), 0, st>>>(a);
 }
 
+template <int XT>
+void go_x(const NormArgs& a, hipStream_t st) {
+  if (a.r_type < 0)
+    go<XT, -1>(a, st);
+  else if (a.r_type == TERN_F32)
+    go<XT, TERN_F32>(a, st);
+  else
+    go<XT, TERN_BF16>(a, st);
+}
+
 }  // namespace
 
 int launch_rmsnorm(const NormArgs& a, void* stream) {
   hipStream_t st = (hipStream_t)stream;
   if (a.x_type == TERN_F32)
-    a.r_type < 0 ? go<TERN_F32, -1>(a, st) : a.r_type == TERN_F32 ? go<TERN_F32, TERN_F32>(a, st) : go<TERN_F32, TERN_BF16>(a, st);
+    go_x<TERN_F32>(a, st);
   else
-    a.r_type < 0 ? go<TERN_BF16, -1>(a, st) : a.r_type == TERN_F32 ? go<TERN_BF16, TERN_F32>(a, st) : go<TERN_BF16, TERN_BF16>(a, st);
+    go_x<TERN_BF16>(a, st);
   return kernel_launched((int)hipGetLastError(), TERN_KERNEL_RMSNORM);
 }
 
