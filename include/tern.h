@@ -602,7 +602,7 @@ typedef enum {
   TERN_KERNEL_KV_APPEND,          /* tern_kv_append */
   TERN_KERNEL_KV_READ,            /* tern_kv_read */
   TERN_KERNEL_KV_ATTN,            /* tern_kv_attn: few rows per kv head, keys and values straight to registers */
-  TERN_KERNEL_KV_ATTN_TILE,       /* tern_kv_attn: more than 32 rows per kv head, operands shared in LDS */
+  TERN_KERNEL_KV_ATTN_TILE,       /* tern_kv_attn: many rows per kv head, operands shared in LDS */
   TERN_KERNEL_KV_ATTN_JOIN,       /* tern_kv_attn: joins the runs of a split key axis */
   TERN_KERNEL_COUNT
 } tern_kernel;

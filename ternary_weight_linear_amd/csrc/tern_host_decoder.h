@@ -171,7 +171,14 @@ constexpr int kComputeUnits = 256;  // of the part that this library is built fo
 tern::KvAttnPlan plan_attn(const tern::KvAttnArgs& a) {
   tern::KvAttnPlan p{};
   const int64_t group = a.q_heads / a.cache.heads, rows = group * a.batch.max_q;
-  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  // Up to 32 rows a kv head the kernel for few rows reads every code once. With
+  // 33 to 64 it reads them twice, which only pays while few (sequence, head)
+  // pairs share the machine (35 rows: 32 us against 39 on one sequence of 32768
+  // tokens and 8 heads, 24 against 27 on 4 of 1500, but 50 against 44 on 16 of
+  // 4096); from 65 on the kernel for many rows wins (65 rows: 47 against 42, 66
+  // against 48).
+  const bool few = rows <= 32 || (rows <= 64 && (int64_t)a.batch.seqs * a.cache.heads <= 64);
+  p.rows = rows <= 16 ? 16 : few ? 32 : 128;
   p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
   const int64_t pages = attn_pages(a, std::min<int64_t>(a.batch.max_q, (p.rows + group - 2) / group + 1));
   const int64_t units = (int64_t)p.row_blocks * a.batch.seqs;

@@ -71,7 +71,8 @@ def run(torch, tl, f, n, hq, scale, seed, window=0, sinks=0):
 @pytest.mark.parametrize("d,heads,hq,n,lens,window,sinks,checked", [
     (64, 8, 16, 1, [600_001], 0, 0, [0]),              # runs of more than 256 pages, few rows
     (64, 8, 16, 1, [600_001], 580_000, 7_000, [0]),    # the same with a window and many sinks
-    (256, 8, 8, 40, [130_003], 0, 0, [0]),             # runs of more than 62 pages, many rows
+    (256, 8, 8, 40, [130_003], 0, 0, [0]),             # two blocks of few rows of one sequence
+    (256, 8, 8, 70, [130_003], 0, 0, [0]),             # runs of more than 62 pages, many rows
     (128, 8, 8, 40, [4_501 - i for i in range(128)], 0, 0, [0, 77]),  # a workgroup a unit, many rows
     (64, 8, 8, 1, [16_900 - 10 * i for i in range(64)], 0, 0, [1, 63]),  # a workgroup a unit, few rows
     (64, 8, 32, 5, [40_000, 3_000, 64, 17_001], 0, 0, [0, 1, 2, 3]),  # two row tiles, runs across sequences
