@@ -182,21 +182,46 @@ tern::KvAttnPlan plan_attn(const tern::KvAttnArgs& a) {
   p.row_blocks = (int)((rows + p.rows - 1) / p.rows);
   const int64_t pages = attn_pages(a, std::min<int64_t>(a.batch.max_q, (p.rows + group - 2) / group + 1));
   const int64_t units = (int64_t)p.row_blocks * a.batch.seqs;
-  // Fewer than two workgroups a compute unit would leave the machine waiting
-  // for the longest of them: then one run a compute unit, of equal lengths.
-  // One workgroup with its loads in flight fills a unit's share of the memory
-  // (256 / 320 / 512 / 768 runs: 64 / 83 / 68 / 72 us for 32 sequences of 1024
-  // to 8192 tokens, 51 / 68 / 57 / 62 us for one of 131072; a workgroup a unit:
-  // 71 us and 875 us); with two units each, 512 of equal lengths, runs and the
-  // second kernel only cost (54 us, against 46 us without).
-  // The kernel for many rows is bound by its arithmetic and wants every
-  // workgroup that the registers admit: 2 a unit at 128 (219 us with 512 runs for
-  // a 1024-token chunk on 8192 keys, 290 with 256, 237 with 768, 282 without)
-  // and 1 at 256 (118 us for windowed chunks, 137 with 512, 135 without).
-  const int held = kComputeUnits * (p.rows <= 32 || a.cache.dim == 256 ? 1 : a.cache.dim == 128 ? 2 : 3);
+  // Equal runs, one workgroup each, or a workgroup a unit. With fewer than two
+  // units a compute unit the longest of them decides, and runs share their
+  // pages evenly, for the price of partial results and of the join. `saved` is
+  // the pages by which that shortens the wait, at most: `lone` units follow each
+  // other on a compute unit without runs, `shared` with them.
   p.least = 8;
-  if (pages > p.least && units <= tern::kKvMaxUnits && units * pages <= (1 << 30) && units * a.cache.heads < 2 * held)
-    p.runs = (int)std::max<int64_t>(1, std::min<int64_t>({held / a.cache.heads, units * pages / p.least, tern::kKvMaxRuns}));
+  const double each = (double)(units * a.cache.heads) / kComputeUnits;  // units a compute unit
+  int held = kComputeUnits;
+  bool pays;
+  if (p.rows <= 32) {
+    // Bound by memory, where one workgroup a compute unit fills its share (256 /
+    // 320 / 512 / 768 runs: 64 / 83 / 68 / 72 us for 32 sequences of 1024 to 8192
+    // tokens). A page costs about (d + 64) / 192 of one at 128; lengths are
+    // taken as three quarters of the bound. Measured, without and with runs: 8
+    // units of 16, 32 and 63 pages 11.0 and 12.5, 15.5 and 12.5, 25.7 and 14.3 us;
+    // 128 units of 16, 32 and 63 pages 11.8 and 20.6, 19.1 and 19.3, 33.1 and
+    // 26.2 us; 64 units of two row tiles and 32 pages, which it cuts, 22.4 and 24.4 us;
+    // 256 units of 128 pages 71 and 60 us; of 63 pages 64 wide 18.9 and
+    // 26.1 us; 512 of 65 pages 46 and 54 us.
+    const double saved = pages * (1 - 0.75 * each) * (a.cache.dim + 64) / 192;
+    pays = saved > 25;
+  } else {
+    // Bound by instruction issue, where two workgroups share a compute unit at up
+    // to 128 (219 us with 512 runs, 290 with 256, 237 with 768 for 320 units of 128
+    // pages) and one fits at 256. Two that share take 1.25 to 1.5 times as long as
+    // one. Measured, without and with runs: 64 units of 62 pages 109 and 47 us, 160
+    // of 8, 31 and 62 pages 21 and 21, 62 and 52, 112 and 76 us; 320 of 16, 32, 64 and
+    // 128 pages 39 and 60, 67 and 72, 139 and 119, 282 and 219 us; 640 of 32 pages 71
+    // and 113 us; at 256: 128 units of 16 and 64 pages 54 and 79, 169 and 110 us, 384
+    // of 31 pages 105 and 163 us, 288 of 20 window pages 135 and 106 us.
+    const bool wide = a.cache.dim == 256;
+    const double mean = a.window ? pages : std::max(0.0, pages - a.batch.max_q / (2.0 * TERN_KV_PAGE));
+    const double lone = wide ? std::ceil(each) : each <= 1 ? 1 : 1.25;
+    const double saved = mean * (lone - each * (wide ? 1 : 0.75));
+    if (!wide) held = 2 * kComputeUnits;
+    pays = each < 2 && saved > 12;
+  }
+  if (pays && pages > p.least && units <= tern::kKvMaxUnits && units * pages <= (1 << 30))
+    p.runs = (int)std::max<int64_t>(
+        1, std::min<int64_t>({held / a.cache.heads, units * pages / p.least, tern::kKvMaxRuns}));
   return p;
 }
 
