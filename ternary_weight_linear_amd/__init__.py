@@ -581,6 +581,13 @@ def _empty(shape, dtype, device, stream):
         return _torch().empty(shape, dtype=dtype, device=device)
 
 
+def _empty_like(t, dtype, stream):
+    """A contiguous output of t's shape for a call on `stream`."""
+    if stream is None and t.is_contiguous():
+        return _torch().empty_like(t, dtype=dtype)  # a third less of the host's time than empty()
+    return _empty(t.shape, dtype, t.device, stream)
+
+
 def _rows(t, name, shape, device):
     """Checks a device matrix (or a matrix of heads) whose rows may lie apart:
     float32 or bfloat16, its shape and device, each row contiguous. Returns
@@ -663,7 +670,7 @@ def rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, strea
     residual_out (default: the residual itself) in the residual's type."""
     made = y is None
     if made:
-        y = _empty(x.shape, _torch().bfloat16, x.device, stream)
+        y = _empty_like(x, _torch().bfloat16, stream)
     _norm(x, weight, eps, residual, residual_out, None, None, "row_major", y, stream, made)
     return y
 
@@ -674,7 +681,7 @@ def rmsnorm_s8(x, weight, eps=1e-6, residual=None, residual_out=None, q=None, sc
     [T]), as linear_s8_q takes them; `y` (bf16) is written too when given."""
     made = q is None and scale is None and y is None
     if q is None:
-        q = _empty(x.shape, _torch().int8, x.device, stream)
+        q = _empty_like(x, _torch().int8, stream)
     if scale is None:
         scale = _empty(x.shape[:1], _torch().float32, x.device, stream)
     _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream, made)
@@ -729,6 +736,7 @@ class KVBatch:
         self._struct = _KvBatch(q_begin.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), seqs, self.max_q,
                                 self.max_kv, width)
         self._ref = ctypes.byref(self._struct)
+        self._workspace = {}  # sizes of a call -> workspace bytes
 
 
 class Rope:
@@ -811,9 +819,9 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Ro
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
-        one = positions.dim() == 1
-        axes = 1 if one else positions.shape[0]
-        _dev(positions, _torch().int32, "positions", (tokens,) if one else (axes, tokens), device)
+        size = positions.shape
+        axes = 1 if len(size) == 1 else size[0]
+        _dev(positions, _torch().int32, "positions", (tokens,) if len(size) == 1 else (axes, tokens), device)
         if rope.device != device:
             raise ValueError(f"rope is on {rope.device}, the cache on {device}")
         r, pp = rope._ref(axes), positions.data_ptr()
@@ -844,9 +852,13 @@ def kv_read(cache: KVCache, batch: KVBatch, rows: int, k_out=None, v_out=None, s
 
 def kv_attn_workspace_bytes(cache: KVCache, batch: KVBatch, tokens: int, q_heads: int, window: int = 0,
                             sinks: int = 0) -> int:
-    n = lib().tern_kv_attn_workspace_bytes(cache._ref, batch._ref, tokens, q_heads, window, sinks)
-    if n == ctypes.c_size_t(-1).value:
-        raise TernError(2, lib().tern_last_error().decode())
+    sizes = (cache.heads, cache.d, tokens, q_heads, window, sinks)
+    n = batch._workspace.get(sizes)
+    if n is None:
+        n = lib().tern_kv_attn_workspace_bytes(cache._ref, batch._ref, tokens, q_heads, window, sinks)
+        if n == ctypes.c_size_t(-1).value:
+            raise TernError(2, lib().tern_last_error().decode())
+        batch._workspace[sizes] = n
     return n
 
 
@@ -855,10 +867,7 @@ def kv_attn_workspace(cache: KVCache, batch: KVBatch, tokens: int, q_heads: int,
     """A workspace for kv_attn calls of these sizes (None if they need none),
     for a caller that keeps one from call to call."""
     n = kv_attn_workspace_bytes(cache, batch, tokens, q_heads, window, sinks)
-    if n == 0:
-        return None
-    with _on(stream):
-        return _torch().empty((n,), dtype=_torch().uint8, device=cache.device)
+    return None if n == 0 else _empty((n,), _torch().uint8, cache.device, stream)
 
 
 def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, sinks: int = 0, out=None,
@@ -876,7 +885,7 @@ def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, si
         raise TypeError(f"q must be bfloat16, got {q.dtype}")
     _same_device(batch, cache)
     if out is None:
-        out = _empty(shape, q.dtype, device, stream)
+        out = _empty_like(q, q.dtype, stream)
     else:
         _dev(out, q.dtype, "out", shape, device)
     if workspace is None:
