@@ -106,3 +106,39 @@ def test_runs_over_sequences_without_tokens(torch, tl, group):  # noqa: F811
     assert not got[qb[1]:qb[2]].any() and not got[qb[6]:qb[7]].any()
     rows = np.concatenate([np.arange(qb[a], qb[a + 1]) for a in used])
     check_attention(f, q[rows], out[torch.from_numpy(rows).to("cuda:0")], [ns[a] for a in used], 0.125)
+
+
+@pytest.mark.parametrize("d,n,group,window", [(128, 200, 1, 0), (256, 60, 3, 0), (256, 7, 4, 0), (128, 1, 5, 3000)])
+def test_graph_of_every_kernel(torch, tl, d, n, group, window):  # noqa: F811
+    """Captured calls (operands in more than 64 KiB of LDS, runs and their join
+    among them) replay with new lengths and queries as the eager calls do."""
+    f = Random(torch, tl, d + n, [5_003, 640, 2_111], 2, d)
+    batch = f.batch(torch, tl, n)
+    g = torch.Generator(device="cuda:0")
+    g.manual_seed(5)
+    qs = [torch.randn((3 * n, 2 * group, d), device="cuda:0", generator=g).bfloat16() for _ in range(4)]
+    lens = [[5_003, 640, 2_111], [4_100, 600, 64 + n], [n, 321, 2_000], [5_000, 639, 1_999]]
+    ws = tl.kv_attn_workspace(f.cache, batch, 3 * n, 2 * group, window, 2)
+
+    def call(q):
+        return tl.kv_attn(q, f.cache, batch, d ** -0.5, window=window, sinks=2, workspace=ws)
+
+    def at(i):
+        batch.kv_len.copy_(torch.tensor(lens[i], dtype=torch.int32))
+
+    eager = []
+    for i, q in enumerate(qs):
+        at(i)
+        eager.append(call(q).clone())
+    cur = qs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = call(cur)
+    for i in (1, 3, 0, 2, 1):
+        at(i)
+        cur.copy_(qs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager[i]), i
+        assert torch.equal(call(qs[i]), eager[i]), i
