@@ -443,6 +443,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
     }
 
     for (int base = begin; base < end;) {
+      ks += ks - ks;  // an infinite scale becomes NaN, which the bound of the factor lets through
       vs = vs < kLeastScale ? kLeastScale : vs;
       const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / (vs * kPScale);
       for (int i = 0; i < steps; ++i) {
@@ -631,6 +632,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
       if (id >= 0) {
         const int64_t ph = (int64_t)id * heads + head;
         ks = a.cache.k_scale[ph];
+        ks += ks - ks;  // an infinite scale becomes NaN, which the bound of the factor lets through
         vs = a.cache.v_scale[ph];
       }
       vs = vs < kLeastScale ? kLeastScale : vs;

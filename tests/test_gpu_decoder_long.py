@@ -142,3 +142,19 @@ def test_graph_of_every_kernel(torch, tl, d, n, group, window):  # noqa: F811
         torch.cuda.synchronize()
         assert torch.equal(out, eager[i]), i
         assert torch.equal(call(qs[i]), eager[i]), i
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("which,bad", [(0, float("inf")), (0, float("nan")), (1, float("inf")), (1, float("nan"))])
+def test_scales_that_are_not_finite(torch, tl, n, which, bad):  # noqa: F811
+    """A page whose scale is not finite (it holds a value that was not) makes
+    exactly the rows NaN that see it, of its head."""
+    f = Random(torch, tl, 7, [700, 700], 2, 128)
+    q, clean = run(torch, tl, f, n, 10, 0.09, 3)
+    page = int(f.table[1, 10])  # keys 640 .. 699 of the second sequence
+    (f.cache.k_scale, f.cache.v_scale)[which][page, 1] = bad
+    _, out = run(torch, tl, f, n, 10, 0.09, 3)
+    sees = torch.zeros((2 * n, 10), dtype=torch.bool, device="cuda:0")
+    sees[n + max(0, 640 - (700 - n)):, 5:] = True
+    assert torch.equal(torch.isnan(out).all(2), sees) and torch.equal(torch.isnan(out).any(2), sees)
+    assert torch.equal(out[~sees], clean[~sees])
