@@ -46,11 +46,13 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr float kNone = -__builtin_inff();
 constexpr float kLeastScale = 0x1p-100f;  // value scales below count as this
 constexpr float kPScale = 0x1p15f;        // of p' in fp16
-// Largest factor from a product of codes (below 2^16) to its score in powers
-// of two: scores past 2^22 have no fp32 fraction left to tell keys apart, and
-// bounding them keeps the rounding of a maximum below half a power of two, so
-// p' stays in fp16.
-constexpr float kMostFactor = 64.f;
+// With a factor f from a product of codes (at most 2^16) to its score in powers
+// of two up to this, scores stay below 2^22 and the rounding of a maximum below
+// half a power of two, so p' stays in fp16. Steeper rows subtract the page's
+// maximum from the products first.
+constexpr float kSteep = 64.f;
+// Largest such factor: products times this are finite.
+constexpr float kMostFactor = 0x1p111f;
 
 // fp16 of the four codes of a dword, exactly.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -77,6 +79,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_waitcnt(0xC07F);  // vmcnt 63 (no wait), expcnt 7, lgkmcnt 0
   asm volatile("s_barrier" ::: "memory");
+}
+
+// x, but what is computed from it stays where it stands: addresses of results
+// are not made ahead of the page loop, whose registers they would take.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
 // Maximum and sum over the four lanes that share lane & 15: the two halves
@@ -257,6 +266,13 @@ struct Queries {
           }
     }
   }
+  // Whether some row's factor with key scale k is above kSteep.
+  __device__ __forceinline__ bool steep(float k) const {
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) any |= k * factor[t] > kSteep;
+    return __any(any);
+  }
 };
 
 // What a page multiplies with: key scale, log2 of the value scale w and
@@ -269,7 +285,8 @@ struct PageScales {
 // Softmax of a page's scores s for the 16 rows of one tile: running maximum M
 // and sum L, the factor alpha for what was summed before, and the second
 // product's operands p. MASKED: some row does not see the whole page.
-template <bool MASKED>
+// STEEP: some row's factor may be above kSteep.
+template <bool MASKED, bool STEEP>
 __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w, float factor, int pos, int j0, int g,
                                              int window, int sinks, float& M, float& L, float& alpha, f16x8 (&p)[2]) {
   float f = w.k * factor;
@@ -295,7 +312,19 @@ __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w,
   const float base = Mn == kNone ? 0.f : Mn;
   alpha = __builtin_amdgcn_exp2f(M - base);
   M = Mn;
-  const float add = (w.log_v - base) + 15.f;  // p' in fp16 stands times 2^15
+  float add = (w.log_v - base) + 15.f;  // p' in fp16 stands times 2^15
+  if constexpr (STEEP) {
+    // (s - mx) f + (top - base) has two terms that are never positive, whatever
+    // f is. Rows with a smaller factor keep their form, so that no row's result
+    // depends on its neighbours.
+    const bool steep = f > kSteep;
+    const float r = steep && mx != kNone ? mx : 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[b][e] -= r;
+    add = steep ? (top - base) + 15.f : add;
+  }
   float sum = 0.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
@@ -483,11 +512,14 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
                            (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
         f16x8 pf[NT][2];
         float alpha[NT];
+        // The form for steep rows always: its 20 instructions a tile cost nothing
+        // beside the loads, a branch to it cost registers (16 x 4 tokens: 30.0 us
+        // against 31.5; the other cases within 0.5 %).
         auto softmax = [&](auto masked) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            page_softmax<decltype(masked)::value>(s[t], w, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
-                                                  alpha[t], pf[t]);
+            page_softmax<decltype(masked)::value, true>(s[t], w, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
+                                                        alpha[t], pf[t]);
         };
         if (whole)
           softmax(std::false_type{});
@@ -525,6 +557,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
     for (int t = 0; t < NT; ++t) L[t] = group_sum(L[t]);
 
     // Join the four waves: 2 and 3 into 0 and 1, then 1 into 0.
+    const int at = here(lane), n1 = at & 15, g1 = at >> 4;
 #pragma unroll
     for (int half = 2; half >= 1; half >>= 1) {
       float* slot = lds + wave % half * kSlot;
@@ -533,22 +566,22 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int h = 0; h < HT; ++h) *(f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) = o[t][h];
-          if (g == 0) ml[16 * t + n] = M[t], ml[R + 16 * t + n] = L[t];
+          for (int h = 0; h < HT; ++h) *(f32x4*)(slot + ((t * HT + h) * 64 + at) * 4) = o[t][h];
+          if (g1 == 0) ml[16 * t + n1] = M[t], ml[R + 16 * t + n1] = L[t];
         }
       }
       __syncthreads();
       if (wave < half) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float m2 = ml[16 * t + n], l2 = ml[R + 16 * t + n];
+          const float m2 = ml[16 * t + n1], l2 = ml[R + 16 * t + n1];
           const float Mn = fmaxf(M[t], m2), b = Mn == kNone ? 0.f : Mn;
           const float x = __builtin_amdgcn_exp2f(M[t] - b), y = __builtin_amdgcn_exp2f(m2 - b);
           M[t] = Mn;
           L[t] = L[t] * x + l2 * y;
 #pragma unroll
           for (int h = 0; h < HT; ++h)
-            o[t][h] = o[t][h] * x + *(const f32x4*)(slot + ((t * HT + h) * 64 + lane) * 4) * y;
+            o[t][h] = o[t][h] * x + *(const f32x4*)(slot + ((t * HT + h) * 64 + at) * 4) * y;
         }
       }
       __syncthreads();
@@ -560,12 +593,12 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
       float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * R * D + slot * R * 2;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const int r = r0 + 16 * t + n;
+        const int r = r0 + 16 * t + n1;
         if (r >= rows) continue;
         if (whole)
-          write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g);
+          write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g1);
         else
-          write_part<D>(po, pm, o[t], M[t], L[t], 16 * t + n, g);
+          write_part<D>(po, pm, o[t], M[t], L[t], 16 * t + n1, g1);
       }
     }
     if (!plan.runs) return;
@@ -732,16 +765,18 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
                          (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
       f16x8 pf[NT][2];
       float alpha[NT];
-      auto softmax = [&](auto masked) {
+      auto softmax = [&](auto masked, auto steep) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          page_softmax<decltype(masked)::value>(s[t], ps, q.factor[t], q.pos[t], j0, g, a.window, a.sinks, M[t], L[t],
-                                                alpha[t], pf[t]);
+          page_softmax<decltype(masked)::value, decltype(steep)::value>(s[t], ps, q.factor[t], q.pos[t], j0, g, a.window,
+                                                                        a.sinks, M[t], L[t], alpha[t], pf[t]);
       };
-      if (whole)
-        softmax(std::false_type{});
+      if (q.steep(ps.k))
+        softmax(std::true_type{}, std::true_type{});
+      else if (whole)
+        softmax(std::false_type{}, std::false_type{});
       else
-        softmax(std::true_type{});
+        softmax(std::true_type{}, std::false_type{});
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         if (__any(alpha[t] != 1.f)) {  // a maximum moved (or a row is NaN)
@@ -761,18 +796,19 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
 #pragma unroll
     for (int t = 0; t < NT; ++t) L[t] = group_sum(L[t]);
 
+    const int at = here(lane), n1 = at & 15, g1 = at >> 4;
     const bool whole = begin == 0 && end == pages.count;
     const int64_t slot = ((int64_t)head * plan.runs + w) * 2 + (begin == 0);
     float* po = ws + ws_head(a, plan) + slot * R * D;
     float* pm = ws + ws_head(a, plan) + (int64_t)heads * plan.runs * 2 * R * D + slot * R * 2;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = r0 + 16 * t + n;
+      const int r = r0 + 16 * t + n1;
       if (r >= rows) continue;
       if (whole)
-        write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g);
+        write_row<D>(a, o[t], L[t], (int64_t)(seq.row0 + r / group) * a.q_heads + head * group + r % group, g1);
       else
-        write_part<D>(po, pm, o[t], M[t], L[t], 32 * wave + 16 * t + n, g);
+        write_part<D>(po, pm, o[t], M[t], L[t], 32 * wave + 16 * t + n1, g1);
     }
     if (!plan.runs) return;
     from += end - begin;
