@@ -340,7 +340,9 @@ __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w,
 #pragma unroll
     for (int e = 0; e < 4; ++e) p[b >> 1][4 * (b & 1) + e] = v[e];
   }
-  L = __builtin_fmaf(L, alpha, sum * w.inv_v);
+  float part = sum * w.inv_v;
+  if constexpr (MASKED) part = sum == 0.f ? 0.f : part;  // a row that sees nothing here, where inv_v is NaN
+  L = __builtin_fmaf(L, alpha, part);
 }
 
 __device__ __forceinline__ float lane_float(float v, int lane) {

@@ -1,0 +1,36 @@
+"""Page scales at the ends of their range: infinite and NaN ones beside rows
+that do not see the page."""
+from __future__ import annotations
+
+import pytest
+
+from tests.test_gpu_decoder import tl, torch  # noqa: F401 (fixtures)
+from tests.test_gpu_decoder_long import Random, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("which,bad", [(0, float("inf")), (0, float("nan")), (1, float("inf")), (1, float("nan"))])
+@pytest.mark.parametrize("n,length,page,window,kernels", [
+    (4, 642, 10, 0, ["kv_attn"]),                            # two rows before the page, two in it
+    (40, 660, 10, 0, ["kv_attn_tile"]),
+    (4, 357, 3, 100, ["kv_attn"]),                           # two rows see the page's last keys, two have left it
+    (40, 370, 3, 100, ["kv_attn_tile"]),
+    (4, 20_034, 313, 0, ["kv_attn", "kv_attn_join"]),
+    (40, 8_980, 140, 0, ["kv_attn_tile", "kv_attn_join"]),
+])
+def test_scales_that_are_not_finite_stay_out_of_rows_that_do_not_see_them(torch, tl, n, length, page, window, kernels,  # noqa: F811
+                                                                         which, bad):
+    f = Random(torch, tl, length, [length, 300], 2, 128)
+    q, clean = run(torch, tl, f, n, 10, 0.09, 3, window)
+    at = int(f.table[0, page])
+    (f.cache.k_scale, f.cache.v_scale)[which][at, 1] = bad
+    _, out = run(torch, tl, f, n, 10, 0.09, 3, window)
+    assert tl.last_kernels() == kernels
+    pos = torch.arange(length - n, length, device="cuda:0")
+    seen = (pos >= 64 * page) & ((pos < 64 * page + 63 + window) if window else True)
+    assert seen.any() and not seen.all()
+    sees = torch.zeros((2 * n, 10), dtype=torch.bool, device="cuda:0")
+    sees[:n, 5:] = seen[:, None]
+    assert torch.equal(torch.isnan(out).all(2), sees) and torch.equal(torch.isnan(out).any(2), sees)
+    assert torch.equal(out[~sees], clean[~sees])
