@@ -48,7 +48,7 @@ __device__ __forceinline__ PageSpan page_span(const KvBatch& b, int64_t pages, i
   r.kept = false;
   const int q0 = b.q_begin[s], q1 = b.q_begin[s + 1];
   const int kv = b.kv_len[s];
-  if (q0 < 0 || q1 > tokens || kv < 0 || kv > b.max_kv) return r;
+  if (q0 < 0 || q1 < q0 || q1 > tokens || kv < 0 || kv > b.max_kv) return r;  // q1 - q0 below does not wrap
   const int n = q1 - q0;
   if (n <= 0 || n > b.max_q || n > kv) return r;
   const int start = kv - n;
