@@ -37,7 +37,9 @@ tern_status check_kv(const tern_kv_cache* c, const tern_kv_batch* b, int rows, t
   return TERN_OK;
 }
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+// Workgroups of a launch, all of 256 threads: the runtime counts a grid's
+// threads in 32 bits, and of a grid past that it launches the remainder only.
+constexpr int64_t kMaxGrid = 0xffffffffu / 256;
 
 }  // namespace
 
