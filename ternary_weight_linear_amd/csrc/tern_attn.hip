@@ -353,7 +353,7 @@ __device__ __forceinline__ float lane_float(float v, int lane) {
 // consecutive elements of every 16).
 template <int D>
 __device__ __forceinline__ void write_row(const KvAttnArgs& a, const f32x4 (&o)[D / 16], float L, int64_t at, int g) {
-  const float inv = L == 0.f ? 0.f : 1.0f / (L * kPScale);
+  const float inv = L == 0.f ? 0.f : 1.0f / L * (1.0f / kPScale);  // L kPScale may pass fp32
   uint16_t* out = a.out + at * D + 4 * g;
 #pragma unroll
   for (int h = 0; h < D / 16; ++h)
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
     for (int base = begin; base < end;) {
       ks += ks - ks;  // an infinite scale becomes NaN, which the bound of the factor lets through
       vs = vs < kLeastScale ? kLeastScale : vs;
-      const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / (vs * kPScale);
+      const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / vs * (1.0f / kPScale);
       for (int i = 0; i < steps; ++i) {
         // What follows part h in its buffer: part h + 2 of this page or the next one's.
         auto refill = [&](int h) {
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
       }
       vs = vs < kLeastScale ? kLeastScale : vs;
       lv = __builtin_amdgcn_logf(vs);
-      iv = 1.0f / (vs * kPScale);
+      iv = 1.0f / vs * (1.0f / kPScale);
     };
     // The wave's quarter of a page's codes: loads wave, wave + 4, ... of keys
     // and of values. A page that is absent, or past the end, reads as zeros.
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
       o += f[j] * y;
     }
   }
-  const float inv = L == 0.f ? 0.f : 1.0f / (L * kPScale);
+  const float inv = L == 0.f ? 0.f : 1.0f / L * (1.0f / kPScale);  // L kPScale may pass fp32
   *(uint2*)(a.out + at * D + 4 * l) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 

@@ -1,5 +1,5 @@
 """Page scales at the ends of their range: infinite and NaN ones beside rows
-that do not see the page."""
+that do not see the page, value scales near the end of fp32."""
 from __future__ import annotations
 
 import pytest
@@ -34,3 +34,30 @@ def test_scales_that_are_not_finite_stay_out_of_rows_that_do_not_see_them(torch,
     sees[:n, 5:] = seen[:, None]
     assert torch.equal(torch.isnan(out).all(2), sees) and torch.equal(torch.isnan(out).any(2), sees)
     assert torch.equal(out[~sees], clean[~sees])
+
+
+@pytest.mark.parametrize("n,lens,kernels", [(1, [300, 70], ["kv_attn"]), (40, [300, 70], ["kv_attn_tile"]),
+                                            (1, [9_000, 70], ["kv_attn", "kv_attn_join"])])
+@pytest.mark.parametrize("scale,every", [(2.0 ** 112, 1), (2.0 ** 114, 1), (2.0 ** 120, 1), (2.0 ** 113, 3)])
+def test_values_up_to_the_end_of_fp32(torch, tl, n, lens, kernels, scale, every):  # noqa: F811
+    """Pages of huge values, alone and among ordinary ones."""
+    f = Random(torch, tl, n, lens, 2, 128)
+    for s in range(2):
+        f.cache.v_scale[f.table[s, :(lens[s] + 63) // 64:every].long()] = scale
+    q, out = run(torch, tl, f, n, 10, 0.09, 3)
+    assert tl.last_kernels() == kernels
+    for s in range(2):
+        f.check(torch, q, out, s, n, 0.09)
+
+
+@pytest.mark.parametrize("n,heads,hq,kernels", [(1, 2, 4, ["kv_attn", "kv_attn_join"]), (40, 2, 8, ["kv_attn_tile", "kv_attn_join"]),
+                                                (1, 256, 256, ["kv_attn"]), (40, 256, 256, ["kv_attn_tile"])])
+def test_many_keys_of_the_least_value_scale(torch, tl, n, heads, hq, kernels):  # noqa: F811
+    """The sum of weights over values of 2^-100 passes 2^113."""
+    f = Random(torch, tl, n, [20_000, 17_000], heads, 64)
+    f.cache.v_scale.fill_(2.0 ** -100)
+    q = torch.zeros((2 * n, hq, 64), dtype=torch.bfloat16, device="cuda:0")
+    out = tl.kv_attn(q, f.cache, f.batch(torch, tl, n), 0.125)
+    assert tl.last_kernels() == kernels
+    for s in range(2):
+        f.check(torch, q, out, s, n, 0.125)
