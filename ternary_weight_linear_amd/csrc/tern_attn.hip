@@ -310,7 +310,12 @@ __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w,
   const float top = mx == kNone ? kNone : __builtin_fmaf(mx, f, w.log_v);
   const float Mn = fmaxf(M, top);
   const float base = Mn == kNone ? 0.f : Mn;
-  alpha = __builtin_amdgcn_exp2f(M - base);
+  // Of pages whose value scales lie far apart the smaller one's p' vanish beside
+  // the other's, but p' / w does not. So the sum of weights takes alpha in two
+  // steps, and a page far below the maximum raises its p' to at most 2^-100 and
+  // its sum back: neither leaves fp32 on the way.
+  const float root = __builtin_amdgcn_exp2f(0.5f * (M - base));
+  alpha = root * root;
   M = Mn;
   float add = (w.log_v - base) + 15.f;  // p' in fp16 stands times 2^15
   if constexpr (STEEP) {
@@ -325,6 +330,8 @@ __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w,
       for (int e = 0; e < 4; ++e) s[b][e] -= r;
     add = steep ? (top - base) + 15.f : add;
   }
+  const float lift = __builtin_amdgcn_fmed3f((base - top) - 100.f, 0.f, 124.f);
+  add += lift;
   float sum = 0.f;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
@@ -340,9 +347,9 @@ __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w,
 #pragma unroll
     for (int e = 0; e < 4; ++e) p[b >> 1][4 * (b & 1) + e] = v[e];
   }
-  float part = sum * w.inv_v;
+  float part = sum * w.inv_v * __builtin_amdgcn_exp2f(-lift);
   if constexpr (MASKED) part = sum == 0.f ? 0.f : part;  // a row that sees nothing here, where inv_v is NaN
-  L = __builtin_fmaf(L, alpha, part);
+  L = __builtin_fmaf(L * root, root, part);
 }
 
 __device__ __forceinline__ float lane_float(float v, int lane) {
@@ -579,8 +586,10 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
           const float m2 = ml[16 * t + n1], l2 = ml[R + 16 * t + n1];
           const float Mn = fmaxf(M[t], m2), b = Mn == kNone ? 0.f : Mn;
           const float x = __builtin_amdgcn_exp2f(M[t] - b), y = __builtin_amdgcn_exp2f(m2 - b);
+          const float M0 = M[t];
           M[t] = Mn;
-          L[t] = L[t] * x + l2 * y;
+          const float rx = __builtin_amdgcn_exp2f(0.5f * (M0 - b)), ry = __builtin_amdgcn_exp2f(0.5f * (m2 - b));
+          L[t] = L[t] * rx * rx + l2 * ry * ry;
 #pragma unroll
           for (int h = 0; h < HT; ++h)
             o[t][h] = o[t][h] * x + *(const f32x4*)(slot + ((t * HT + h) * 64 + at) * 4) * y;
@@ -865,7 +874,8 @@ __global__ void __launch_bounds__(256) tern_kv_attn_join_kernel(KvAttnArgs a, Kv
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float y = q + j < pieces ? __builtin_amdgcn_exp2f(ml[j].x - b) : 0.f;
-      L = __builtin_fmaf(ml[j].y, y, L);
+      const float ry = q + j < pieces ? __builtin_amdgcn_exp2f(0.5f * (ml[j].x - b)) : 0.f;
+      L = __builtin_fmaf(ml[j].y * ry, ry, L);
       o += f[j] * y;
     }
   }
