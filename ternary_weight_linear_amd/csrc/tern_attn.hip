@@ -253,7 +253,9 @@ struct Queries {
       m = __float_as_uint(group_max(__uint_as_float(min(m, 0x7f800000u))));  // a NaN takes infinity's exponent
       // 2^e <= max|q| < 2^(e+1); rows of zeros and of subnormals take e = -126
       const int e = min(max((int)(m >> 23) - 127, -126), 126);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      // A row with an infinite element has only infinite and NaN scores, so no
+      // result: its operands become NaN, since a score of -inf would pass for hidden.
+      const float down = __uint_as_float(m == 0x7f800000u ? 0x7fc00000u : (uint32_t)(127 - e) << 23);
       factor[t] = scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
       for (int c = 0; c < C; ++c)
