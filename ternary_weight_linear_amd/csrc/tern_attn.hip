@@ -256,7 +256,8 @@ struct Queries {
       // A row with an infinite element has only infinite and NaN scores, so no
       // result: its operands become NaN, since a score of -inf would pass for hidden.
       const float down = __uint_as_float(m == 0x7f800000u ? 0x7fc00000u : (uint32_t)(127 - e) << 23);
-      factor[t] = scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+      // finite, so that a page of zero keys has scores of zero
+      factor[t] = fminf(scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23), 0x1p127f);
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll

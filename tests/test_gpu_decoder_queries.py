@@ -1,4 +1,5 @@
-"""Query rows at the ends of their range."""
+"""Query rows at the ends of their range: infinite elements, and rows whose
+factor alone passes fp32."""
 from __future__ import annotations
 
 import pytest
@@ -33,3 +34,15 @@ def test_rows_of_infinite_queries_are_nan(torch, tl, n, lens, kernels, value, si
     sees[2 * n:] = False
     assert torch.isnan(out[sees]).all()
     assert torch.equal(out[~sees], clean[~sees])
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_pages_of_zero_keys_under_a_factor_past_fp32(torch, tl, n):  # noqa: F811
+    """scale times the row's power of two is past fp32; a page of zero keys still
+    has scores of zero, not 0 * inf."""
+    d, lens = 64, [100]
+    f = Random(torch, tl, 3, lens, 1, d)
+    f.cache.k.zero_()
+    f.cache.k_scale.zero_()
+    q = torch.full((n, 2, d), 3e38, device="cuda:0").bfloat16()
+    out = tl.kv_attn(q, f.cache, f.batch(torch, tl, n), 8.0)
+    f.check(torch, q, out, 0, n, 8.0)
