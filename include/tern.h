@@ -519,6 +519,11 @@ typedef struct {
  * round-half-even(fl(fl(c s_old) / s)); else fl(max|new| / 127). New codes are
  * clamp(round-half-even(fl(x / s)), -127, 127), zero where s is zero.
  * A page that several sequences share must not be appended to (copy it first).
+ * A page's scale never shrinks while it fills, and codes once rounded to a
+ * larger one stay so: tokens that are taken back (a shorter kv_len) leave the
+ * earlier tokens of their first page on the scale that they brought, and values
+ * that are not finite leave them 0 or -127 under a scale that is not. A caller
+ * that may take tokens back keeps a copy of that page and its scales.
  * k, v: [tokens] rows of heads * dim, k_stride and v_stride elements apart;
  * q: rows of q_heads * dim, q_stride apart, or NULL (with q_out); all of
  * `type`. positions: device int32 [axes][tokens] (with rope). Row starts and

@@ -794,7 +794,11 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Ro
     """Appends k, v [tokens, heads, d] (float32 or bfloat16, rows may lie apart,
     as in a fused projection's output) to the cache, k turned by its
     positions; returns q [tokens, q_heads, d] turned and rounded to bf16 (None
-    without q). positions: int32 [axes, tokens] or [tokens]."""
+    without q). positions: int32 [axes, tokens] or [tokens]. A page's scale
+    never shrinks while it fills: tokens taken back by a shorter kv_len leave the
+    earlier ones of their page coarser (lost, if they were not finite), so copy
+    the page first where that matters. q's rows are all written, whatever the
+    batch leaves out."""
     device, d = cache.device, cache.d
     tokens = k.shape[0]
     shape = (tokens, cache.heads, d)
@@ -834,7 +838,9 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, q=None, q_out=None, rope: Ro
 
 def kv_read(cache: KVCache, batch: KVBatch, rows: int, k_out=None, v_out=None, stream=None):
     """(k, v) bf16 [rows, heads, d]: the stored values of every sequence's last
-    q_begin[s + 1] - q_begin[s] tokens."""
+    q_begin[s + 1] - q_begin[s] tokens. Rows that no sequence has, or one that
+    the call leaves out (see tern_kv_batch in tern.h), are not written: they
+    hold what k_out and v_out held, or memory's contents."""
     bf16 = _torch().bfloat16
     shape = (rows, cache.heads, cache.d)
     if k_out is None:
@@ -874,7 +880,10 @@ def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, si
             workspace=None, stream=None):
     """out [tokens, q_heads, d] bf16: attention of q (bf16, rows may lie apart)
     over the cache. A query at position i sees key j <= i, with a window only
-    those with j > i - window or j < sinks; a row that sees none is zero."""
+    those with j > i - window or j < sinks; a row that sees none is zero. Rows
+    that no sequence has, or one whose q_begin the call leaves out (see
+    tern_kv_batch in tern.h), are not written: they hold what out held, or
+    memory's contents."""
     device = cache.device
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, d]")
