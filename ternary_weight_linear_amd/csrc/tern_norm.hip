@@ -110,9 +110,10 @@ __global__ void __launch_bounds__(1024) tern_rmsnorm_kernel(NormArgs a) {
   __syncthreads();
   ss = wsum[0], m = wmax[0];
   for (int w = 1; w < nw; ++w) ss += wsum[w], m = max(m, wmax[w]);
-  const float rho = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  // Without an eps rho is infinite for a token of zeros, and y would be 0 * inf.
+  const float rho = m == 0 ? 0.f : 1.0f / sqrtf(ss / (float)a.K + a.eps);
   const float sc = __uint_as_float(m) / 127.0f;
-  if (threadIdx.x == 0 && a.q) a.act_scale[t] = m == 0 ? 0.f : rho * sc;
+  if (threadIdx.x == 0 && a.q) a.act_scale[t] = rho * sc;
   const Coder coder(sc);
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
