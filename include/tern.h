@@ -435,7 +435,9 @@ typedef enum { TERN_F32 = 0, TERN_BF16 = 1 } tern_dtype;
  *   rho = 1 / sqrt(sum_k h[k]^2 / K + eps);  v[k] = fl(h[k] weight[k]);
  *   y[t][k] = bf16(v[k] rho);
  *   a = fl(max_k |v[k]| / 127);  q[t][k] = clamp(round-half-even(fl(v[k] / a)), -127, 127);
- *   act_scale[t] = fl(rho a); a token of zeros gives scale 0 and zero codes.
+ *   act_scale[t] = fl(rho a); a token of zeros gives scale 0, zero codes and y = 0.
+ * All of it in fp32: where the sum of squares passes fp32 (|h| near 2^60) rho is
+ * 0, where it vanishes (|h| below 2^-75) and eps is 0, infinite.
  * rho cancels in the quotient, so the codes are exact functions of v. q and
  * act_scale (both or neither) are what tern_linear_s8_q takes; y (or NULL) is
  * what tern_linear takes; at least one of q and y is asked for.
