@@ -619,6 +619,12 @@ def _rows(t, name, shape, device):
     return kind, stride[0] if size[0] > 1 else max(row, stride[0])
 
 
+def _int32(n, name):
+    """Checks an argument that C takes in 32 bits (ctypes would drop the others)."""
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}={n} does not fit 32 bits")
+
+
 def _on_gpu(t, name):
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -732,6 +738,8 @@ class KVBatch:
         _dev(kv_len, torch.int32, "kv_len", (seqs,), page_table.device)
         _dev(q_begin, torch.int32, "q_begin", (seqs + 1,), page_table.device)
         self.q_begin, self.kv_len, self.page_table = q_begin, kv_len, page_table
+        _int32(max_q, "max_q")
+        _int32(max_kv, "max_kv")
         self.seqs, self.max_q, self.max_kv, self.device = seqs, int(max_q), int(max_kv), page_table.device
         self._struct = _KvBatch(q_begin.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), seqs, self.max_q,
                                 self.max_kv, width)
@@ -861,6 +869,8 @@ def kv_attn_workspace_bytes(cache: KVCache, batch: KVBatch, tokens: int, q_heads
     sizes = (cache.heads, cache.d, tokens, q_heads, window, sinks)
     n = batch._workspace.get(sizes)
     if n is None:
+        for name, x in (("tokens", tokens), ("q_heads", q_heads), ("window", window), ("sinks", sinks)):
+            _int32(x, name)
         n = lib().tern_kv_attn_workspace_bytes(cache._ref, batch._ref, tokens, q_heads, window, sinks)
         if n == ctypes.c_size_t(-1).value:
             raise TernError(2, lib().tern_last_error().decode())
@@ -885,6 +895,9 @@ def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, si
     tern_kv_batch in tern.h), are not written: they hold what out held, or
     memory's contents."""
     device = cache.device
+    if not (-2 ** 31 <= window < 2 ** 31 and -2 ** 31 <= sinks < 2 ** 31):
+        _int32(window, "window")
+        _int32(sinks, "sinks")
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, d]")
     tokens, heads = q.shape[:2]
