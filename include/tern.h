@@ -466,7 +466,8 @@ tern_status tern_rmsnorm(const void* x, tern_dtype x_type, int64_t x_stride, con
  *   k [pages][heads][64][dim] int8: slot t of a page is its t-th token;
  *   v [pages][heads][dim][64] int8: slot 16 i + 4 g + e at place 16 g + 4 i + e;
  *   k_scale, v_scale [pages][heads].
- * dim is 64, 128 or 256. Codes of slots that hold no token are unspecified.
+ * dim is 64, 128 or 256. Scales are not negative. Codes of slots that hold no
+ * token are unspecified.
  */
 typedef struct {
   int8_t* k;
