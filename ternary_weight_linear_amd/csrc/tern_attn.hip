@@ -285,6 +285,10 @@ struct PageScales {
   bool absent;
 };
 
+// 2^-15 / w. A NaN scale makes the rows NaN that see the page through its
+// logarithm; here it counts as 0, for the rows that do not (0 * NaN).
+__device__ __forceinline__ float weight_of(float w) { return w == w ? 1.0f / w * (1.0f / kPScale) : 0.f; }
+
 // Softmax of a page's scores s for the 16 rows of one tile: running maximum M
 // and sum L, the factor alpha for what was summed before, and the second
 // product's operands p. MASKED: some row does not see the whole page.
@@ -350,9 +354,7 @@ __device__ __forceinline__ void page_softmax(f32x4 (&s)[4], const PageScales& w,
 #pragma unroll
     for (int e = 0; e < 4; ++e) p[b >> 1][4 * (b & 1) + e] = v[e];
   }
-  float part = sum * w.inv_v * __builtin_amdgcn_exp2f(-lift);
-  if constexpr (MASKED) part = sum == 0.f ? 0.f : part;  // a row that sees nothing here, where inv_v is NaN
-  L = __builtin_fmaf(L * root, root, part);
+  L = __builtin_fmaf(L * root, root, sum * w.inv_v * __builtin_amdgcn_exp2f(-lift));
 }
 
 __device__ __forceinline__ float lane_float(float v, int lane) {
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
     for (int base = begin; base < end;) {
       ks += ks - ks;  // an infinite scale becomes NaN, which the bound of the factor lets through
       vs = vs < kLeastScale ? kLeastScale : vs;
-      const float lv = __builtin_amdgcn_logf(vs), iv = 1.0f / vs * (1.0f / kPScale);
+      const float lv = __builtin_amdgcn_logf(vs), iv = weight_of(vs);
       for (int i = 0; i < steps; ++i) {
         // What follows part h in its buffer: part h + 2 of this page or the next one's.
         auto refill = [&](int h) {
@@ -524,9 +526,9 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
                            (!a.window || j0 > pos_max - a.window || j0 + kKvPage <= a.sinks);
         f16x8 pf[NT][2];
         float alpha[NT];
-        // The form for steep rows always: its 20 instructions a tile cost nothing
-        // beside the loads, a branch to it cost registers (16 x 4 tokens: 30.0 us
-        // against 31.5; the other cases within 0.5 %).
+        // The form for steep rows always: its 16 subtractions a tile hide behind the
+        // loads, a branch to it costs registers (16 x 4 tokens: 30.0 us against
+        // 31.5; the other cases within 0.5 %).
         auto softmax = [&](auto masked) {
 #pragma unroll
           for (int t = 0; t < NT; ++t)
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
       }
       vs = vs < kLeastScale ? kLeastScale : vs;
       lv = __builtin_amdgcn_logf(vs);
-      iv = 1.0f / vs * (1.0f / kPScale);
+      iv = weight_of(vs);
     };
     // The wave's quarter of a page's codes: loads wave, wave + 4, ... of keys
     // and of values. A page that is absent, or past the end, reads as zeros.
@@ -785,6 +787,8 @@ __global__ void __launch_bounds__(256, D == 256 ? 1 : 2) tern_kv_attn_tile_kerne
           page_softmax<decltype(masked)::value, decltype(steep)::value>(s[t], ps, q.factor[t], q.pos[t], j0, g, a.window,
                                                                         a.sinks, M[t], L[t], alpha[t], pf[t]);
       };
+      // Bound by issue, so a branch: 1024 tokens on 8192 keys 211 us against 218 with
+      // the form for steep rows always, 3 x 508 tokens with a window 109 against 112.
       if (q.steep(ps.k))
         softmax(std::true_type{}, std::true_type{});
       else if (whole)
