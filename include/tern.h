@@ -559,7 +559,9 @@ tern_status tern_kv_read(const tern_kv_cache* cache, const tern_kv_batch* batch,
  * ws: device, tern_kv_attn_workspace_bytes() bytes for the same arguments
  * (16-byte aligned, any contents; NULL if 0); calls that share it must not
  * overlap.
- * Scores and softmax statistics are fp32; probabilities, times their v scales,
+ * Scores and softmax statistics are fp32; a row of q enters the first product as
+ * fp16 under a power of two of its own (elements below 2^-14 of its largest lose
+ * bits, below 2^-25 all of them); probabilities, times their v scales,
  * enter the product with the codes as fp16 (11 bits, down to 2^-29 of the row's
  * largest). v scales below 2^-100 count as 2^-100; a k scale
  * whose product with scale and a row's largest |q| passes about 2^110 counts

@@ -383,12 +383,12 @@ __device__ __forceinline__ void write_part(float* po, float* pm, const f32x4 (&o
 // takes pages w, w + 4, ... of what the workgroup visits of a unit.
 //
 // Bound by HBM: every code is read once, straight to the registers of the wave
-// that uses it. About 430 vector instructions a page (conversion 320, softmax
-// 110) run beside the 16 KB of a page at d = 128. One workgroup a compute unit
+// that uses it. About 460 vector instructions a page (conversion 320, softmax
+// 140) run beside the 16 KB of a page at d = 128. One workgroup a compute unit
 // with two pages' halves in flight a wave is enough (8 waves a workgroup, or
 // more workgroups, were no faster). One sequence of 131072 tokens: 46 us =
 // 5.8 TB/s (a read of as many bytes without other work: 39 us); 32 sequences
-// of 1024 to 8192 tokens: 55 us = 5.6 TB/s; both + 5 us for the join. 16
+// of 1024 to 8192 tokens: 56 us = 5.5 TB/s; both + 5 us for the join. 16
 // sequences x 4 tokens: 27 us for 80 MB, of which about 10 are the start
 // (lengths, prefix sums, page ids, first codes) and end of a workgroup.
 template <int D, int NT>
@@ -628,12 +628,12 @@ __global__ void __launch_bounds__(256, D * NT <= 64 ? 4 : D * NT <= 256 ? 2 : 1)
 
 // Many query rows: a unit of 128 rows, 32 a wave, whose waves share each
 // page's codes. Bound by instruction issue: a page costs a wave 64 matrix
-// products (1024 cycles), about 320 vector instructions (1400) and 32 LDS
+// products (1024 cycles), about 340 vector instructions (1480) and 32 LDS
 // reads, and they overlap little: leaving out any one of conversion, exp,
 // either product or the LDS reads of a copy gains 6 to 16 % each, and a
 // software pipeline that lays one page's softmax between the next page's
 // products gained 4 % at d = 128 and lost 5 % at 256. 1024 tokens x 40 heads of
-// 128 on 8192 keys: 211 us with the join (763 TFLOP/s; a library fp16 product
+// 128 on 8192 keys: 209 us with the join (769 TFLOP/s; a library fp16 product
 // of 8192^3 runs at 1165), of which the join takes 14. The workgroup turns the codes into fp16 operands once, in LDS
 // (one page ahead: two buffers, one barrier a page), so that the conversion
 // costs a quarter of what it costs a wave by itself; the operands lie in the
