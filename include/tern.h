@@ -484,13 +484,13 @@ typedef struct {
  *   kv_len [seqs]: tokens of the sequence, this call's among them;
  *   page_table [seqs][table_width]: page of its tokens 64 i .. 64 i + 63.
  * max_q and max_kv bound the rows and tokens of a sequence (they size the
- * launch); max_kv <= 64 table_width. The kernels check what they read, so that
- * no array can lead them outside the buffers: a sequence whose q_begin leaves
- * the rows of the call or exceeds max_q is left out (its rows are not
- * written); one whose kv_len is outside [0, max_kv], or (append and read)
- * smaller than its rows of the call, appends and reads nothing and has no keys
- * for the attention; a page outside the cache is not written, and its keys
- * are absent.
+ * launch, which is refused from 2^24 workgroups on); max_kv <= 64 table_width.
+ * The kernels check what they read, so that no array can lead them outside the
+ * buffers: a sequence whose q_begin leaves the rows of the call or exceeds
+ * max_q is left out (its rows are not written); one whose kv_len is outside [0,
+ * max_kv], or (append and read) smaller than its rows of the call, appends and
+ * reads nothing and has no keys for the attention; a page outside the cache is
+ * not written, and its keys are absent.
  */
 typedef struct {
   const int32_t* q_begin;
@@ -559,13 +559,13 @@ tern_status tern_kv_read(const tern_kv_cache* cache, const tern_kv_batch* batch,
  * ws: device, tern_kv_attn_workspace_bytes() bytes for the same arguments
  * (16-byte aligned, any contents; NULL if 0); calls that share it must not
  * overlap.
- * Scores and softmax statistics are fp32; a row of q enters the first product as
- * fp16 under a power of two of its own (elements below 2^-14 of its largest lose
- * bits, below 2^-25 all of them); probabilities, times their v scales,
+ * Scores and softmax statistics are fp32; a row of q enters the first product
+ * as fp16 under a power of two of its own (elements below 2^-14 of its largest
+ * lose bits, below 2^-25 all of them); probabilities, times their v scales,
  * enter the product with the codes as fp16 (11 bits, down to 2^-29 of the row's
- * largest). v scales below 2^-100 count as 2^-100; a k scale
- * whose product with scale and a row's largest |q| passes about 2^110 counts
- * for that row as if it did not.
+ * largest). v scales below 2^-100 count as 2^-100; a k scale whose product with
+ * scale and a row's largest |q| passes about 2^110 is taken for that row as the
+ * one that reaches it.
  * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.
  */
 tern_status tern_kv_attn(const tern_kv_cache* cache, const tern_kv_batch* batch, int tokens,

@@ -16,9 +16,11 @@
 // Codes become fp16 exactly (|code| <= 127): with u = code + 128 in the low
 // byte, the fp16 pattern 0x6400 | u is 1024 + u, and one packed subtraction
 // of 1152 leaves the code. A query row is brought to [1, 2) by a power of two,
-// which keeps its 8 significant bits and every element down to 2^-24 of the
-// largest. Scores are fp32; the key scale, the softmax scale and the row's
-// power of two multiply them in one factor per lane and page.
+// which keeps the 8 significant bits of every element down to 2^-14 of the
+// largest, fewer below, and none from 2^-25 on: an error of at most 2^-25 of the
+// largest times a code, as fp32 makes in the sum. Scores are fp32; the key scale,
+// the softmax scale and the row's power of two multiply them in one factor per
+// lane and page.
 //
 // The value scale w of a page goes into the exponent: with the running
 // maximum M of s + log2(w) (s: scores in powers of two), p' = 2^(s + log2 w -
