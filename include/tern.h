@@ -575,6 +575,117 @@ tern_status tern_kv_attn(const tern_kv_cache* cache, const tern_kv_batch* batch,
 size_t tern_kv_attn_workspace_bytes(const tern_kv_cache* cache, const tern_kv_batch* batch, int tokens,
                                     int q_heads, int window, int sinks);
 
+/* ---- Operators of a decoder's recurrent block between its projections: the
+ * short causal convolution, the selective state space scan, and the norms
+ * around them. ---- */
+
+/*
+ * The sequences of a call whose operators keep a state each, ragged (device
+ * arrays, read when the kernels run):
+ *   begin [seqs + 1]: rows begin[s] .. begin[s+1]-1 of the call's token
+ *     matrices belong to sequence s, in order;
+ *   src [seqs]: the slot of the state pool that holds the state before them;
+ *     one outside the pool (-1) stands for a state of zeros;
+ *   dst [seqs]: the slot that takes the state after them; one outside the pool:
+ *     it is not kept.
+ * max_q bounds the rows of a sequence. src and dst may be the same slot. A slot
+ * that one sequence writes must not be read or written by another sequence of
+ * the call. A sequence without rows, or whose begin leaves the rows of the call
+ * or exceeds max_q, is left out: its rows and its slot are not written.
+ */
+typedef struct {
+  const int32_t* begin;
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t seqs, max_q;
+} tern_state_batch;
+
+/*
+ * Short causal convolution over the tokens of every channel (device, async):
+ *   y[t][c] = act(bias[c] + sum_{i < width} weight[c][i] x[t - (width - 1) + i][c]),
+ * act(v) = v / (1 + exp(-v)) with silu, else v; inputs before a sequence's first
+ * row come from its state. Sums in fp32 in the order of i, from the bias on.
+ * state: device, of x's type, [slots][width - 1][channels], the last inputs,
+ * oldest first; 16-byte aligned. A prompt in pieces gives the values of the whole.
+ * x: [rows] of `channels`, x_stride elements apart, of `type`. weight
+ * [channels][width] and bias [channels] (or NULL): of weight_type. y: bf16 rows
+ * y_stride apart. width 2, 3 or 4; channels a multiple of 8 up to 2^20; pointers
+ * and rows 16-byte aligned. y does not overlap x. Errors as tern_rmsnorm.
+ */
+tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void* x, tern_dtype type,
+                             int64_t x_stride, int channels, int width, const void* weight, const void* bias,
+                             tern_dtype weight_type, int silu, void* state, int slots, void* y_bf16,
+                             int64_t y_stride, void* stream);
+
+/*
+ * Selective state space scan (device, async). Head h of `heads` keeps a state S
+ * [state_dim][dim] and takes B and C of group h / (heads / groups):
+ *   D[t] = dt[t][h] + dt_bias[h] (dt_bias NULL: 0), with softplus log(1 + exp(.)) of it;
+ *   S[t][n][p] = exp(D[t] a[h]) S[t-1][n][p] + D[t] B[t][n] x[t][p];
+ *   y[t][p] = sum_n C[t][n] S[t][n][p] + d[h] x[t][p] (d NULL: without the last term).
+ * x: bf16 [rows] of heads * dim, x_stride elements apart; b, c: bf16 [rows] of
+ * groups * state_dim, b_stride and c_stride apart; dt: [rows] of heads, dt_stride
+ * apart, of dt_type; a, d, dt_bias: fp32 [heads]; a is finite, and D a <= 0 where the
+ * recurrence is stable. state: fp32 [slots][heads][state_dim][dim]; y: bf16
+ * [rows][heads][dim].
+ * dim is 32, 64 or 128, state_dim 64, 128 or 256. x, b, c, their rows, state and y
+ * are 16-byte aligned. y overlaps no input.
+ * States are fp32 throughout. Calls with more than 16 rows a sequence work in
+ * blocks of 64 rows through matrix products of bf16 operands with fp32 sums: B, C
+ * and x enter as they are, weighted x and the state as sums of two bf16 numbers (16
+ * bits), the weights inside a block likewise. There, a value that is not finite
+ * makes the results that depend on it infinite or NaN; no other rows or channels.
+ * ws: device, tern_scan_workspace_bytes() bytes for the same arguments (16-byte
+ * aligned, any contents; NULL if 0); calls that share it must not overlap.
+ * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.
+ */
+tern_status tern_scan(const tern_state_batch* batch, int rows, int heads, int dim, int groups, int state_dim,
+                      const void* x_bf16, int64_t x_stride, const void* b_bf16, int64_t b_stride,
+                      const void* c_bf16, int64_t c_stride, const void* dt, tern_dtype dt_type, int64_t dt_stride,
+                      const float* dt_bias, int softplus, const float* a, const float* d, float* state, int slots,
+                      void* y_bf16, void* ws, size_t ws_bytes, void* stream);
+/* (size_t)-1 if the arguments are invalid (tern_last_error says why). */
+size_t tern_scan_workspace_bytes(const tern_state_batch* batch, int rows, int heads, int dim, int groups,
+                                 int state_dim);
+
+/*
+ * RMS norm over groups of channels with a gate (device, async). Per token t,
+ * g(z) = z / (1 + exp(-z)):
+ *   u[k] = x[t][k] g(z[t][k]) with gate_first, else x[t][k];
+ *   rho = 1 / sqrt(sum of u^2 over k's group / group + eps);
+ *   v[k] = u[k] weight[k] rho, times g(z[t][k]) without gate_first;
+ *   y[t][k] = bf16(v[k]);
+ *   act_scale[t] = fl(max_k |v[k]| / 127);
+ *   q[t][k] = clamp(round-half-even(fl(v[k] / act_scale[t])), -127, 127);
+ * a token of zeros gives scale 0, zero codes and y = 0. All of it in fp32. x
+ * and z: [T] rows of K, x_stride and z_stride elements apart, of x_type and
+ * z_type. weight: [K] of weight_type. `group` divides K and is a multiple of 16, of
+ * 64 for TERN_Q_OPERAND_ORDER. Outputs and the rest as tern_rmsnorm.
+ */
+tern_status tern_rmsnorm_gated(const void* x, tern_dtype x_type, int64_t x_stride, const void* z,
+                               tern_dtype z_type, int64_t z_stride, const void* weight, tern_dtype weight_type,
+                               int group, int gate_first, float eps, int T, int k, int8_t* q, float* act_scale,
+                               tern_q_layout layout, void* y_bf16, int64_t y_stride, void* stream);
+
+/*
+ * The norm behind a block, the residual's addition with a scale and a gate, and
+ * the norm in front of the next block (device, async). Per token t:
+ *   p[k] = x[t][k] post_weight[k] / sqrt(sum_k x[t][k]^2 / K + eps);
+ *   h[k] = residual[t][k] + scale gate[k] p[k] (gate NULL: 1; gate_stride > 0:
+ *          gate[t][k], rows gate_stride apart), rounded to the residual's type and
+ *          written to residual_out[t];
+ *   q, act_scale and y from h and weight as tern_rmsnorm makes them.
+ * Without a weight (NULL; then q, act_scale and y are NULL too) it ends with h.
+ * post_weight and weight: [K] of weight_type; gate: of gate_type, gate_stride 0
+ * or at least K; scale finite. The rest as tern_rmsnorm.
+ */
+tern_status tern_rmsnorm_post(const void* x, tern_dtype x_type, int64_t x_stride, const void* post_weight,
+                              const void* gate, tern_dtype gate_type, int64_t gate_stride, float scale,
+                              const void* residual, int64_t residual_stride, void* residual_out,
+                              int64_t residual_out_stride, tern_dtype residual_type, const void* weight,
+                              tern_dtype weight_type, float eps, int T, int k, int8_t* q, float* act_scale,
+                              tern_q_layout layout, void* y_bf16, int64_t y_stride, void* stream);
+
 /* Rung probe: number of kernel launches per rung since the last reset,
  * counted at the launch site of the kernel that actually ran. */
 void tern_probe_snapshot(uint64_t out[TERN_RUNG_COUNT]);
@@ -617,6 +728,10 @@ typedef enum {
   TERN_KERNEL_KV_ATTN,            /* tern_kv_attn: few rows per kv head, keys and values straight to registers */
   TERN_KERNEL_KV_ATTN_TILE,       /* tern_kv_attn: many rows per kv head, operands shared in LDS */
   TERN_KERNEL_KV_ATTN_JOIN,       /* tern_kv_attn: joins the runs of a split key axis */
+  TERN_KERNEL_CAUSAL_CONV,        /* tern_causal_conv */
+  TERN_KERNEL_SCAN_STEP,          /* tern_scan: token by token, the state in registers */
+  TERN_KERNEL_RMSNORM_GATED,      /* tern_rmsnorm_gated */
+  TERN_KERNEL_RMSNORM_POST,       /* tern_rmsnorm_post */
   TERN_KERNEL_COUNT
 } tern_kernel;
 
@@ -625,7 +740,8 @@ void tern_kernel_probe_snapshot(uint64_t out[TERN_KERNEL_COUNT]);
 /* Bit i set: kernel i was launched by the most recent successful call on this
  * thread of tern_linear, tern_linear_s8_q, tern_debug_s8_acc,
  * tern_quant_act_s8, tern_quant_act_s8_rot, tern_stream_read, tern_rmsnorm,
- * tern_kv_append, tern_kv_read or tern_kv_attn (0 before any). With TERN_DEBUG=1 the rung line of tern_linear names them too. */
+ * tern_kv_append, tern_kv_read, tern_kv_attn, tern_causal_conv, tern_scan,
+ * tern_rmsnorm_gated or tern_rmsnorm_post (0 before any). With TERN_DEBUG=1 the rung line of tern_linear names them too. */
 uint64_t tern_last_kernels(void);
 /* Host-only dry run of the dispatcher (no HIP call): the kernel-id bit mask
  * (as tern_last_kernels) that tern_linear(T, N, K, G, rung) on weights of

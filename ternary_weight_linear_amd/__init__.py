@@ -18,6 +18,11 @@ Entry points mirror the C ABI in ``include/tern.h``:
 * ``KVCache`` / ``KVBatch`` / ``Rope`` -- the 8-bit paged cache, a call's sequences, rotary positions
 * ``kv_append`` / ``kv_read``  -- new tokens into the cache (rotary q and k), stored values out of it
 * ``kv_attn`` / ``kv_attn_workspace`` -- attention over the cache (window and sinks optional)
+* ``StateBatch``               -- a call's sequences and the state slots they read and leave
+* ``causal_conv``              -- short causal convolution with its state
+* ``scan`` / ``scan_workspace`` -- selective state space scan (single tokens, drafts, prompts)
+* ``rmsnorm_gated`` / ``rmsnorm_gated_s8`` -- RMS norm over groups with a gate
+* ``rmsnorm_post`` / ``rmsnorm_post_s8`` -- norm behind a block, scaled residual addition, next norm
 * ``probe_snapshot`` / ``probe_reset`` / ``last_rung`` / ``resolve_rung``
 * ``kernel_probe_snapshot`` / ``last_kernels`` -- which kernels ran
 
@@ -54,7 +59,7 @@ KERNELS = ("quant_s8", "quant_s8_row", "quant_s8_rot", "gemv_limb", "gemv_bf16",
            "smallt_wave", "smallt_tile", "smallt_tile_reduce", "b16_prefill", "s8_mma",
            "s8_reduce", "s8_row", "s8_acc_export", "stream_read", "gemv_t5", "chain",
            "smallt_narrow", "rmsnorm", "kv_append", "kv_read", "kv_attn", "kv_attn_tile",
-           "kv_attn_join")
+           "kv_attn_join", "causal_conv", "scan_step", "rmsnorm_gated", "rmsnorm_post")
 
 # Symbols declared in include/tern.h (checked by the host tests).
 EXPORTS = ("tern_packed_code_bytes", "tern_scale_count", "tern_pack", "tern_unpack",
@@ -66,7 +71,8 @@ EXPORTS = ("tern_packed_code_bytes", "tern_scale_count", "tern_pack", "tern_unpa
            "tern_plan_kernels", "tern_linear_noalloc", "tern_packed_code_bytes_t5", "tern_pack_t5",
            "tern_unpack_t5", "tern_chain_table_bytes", "tern_chain_counter_bytes", "tern_chain_build",
            "tern_linear_chain", "tern_rmsnorm", "tern_kv_append", "tern_kv_read", "tern_kv_attn",
-           "tern_kv_attn_workspace_bytes")
+           "tern_kv_attn_workspace_bytes", "tern_causal_conv", "tern_scan", "tern_scan_workspace_bytes",
+           "tern_rmsnorm_gated", "tern_rmsnorm_post")
 
 
 class TernError(RuntimeError):
@@ -108,6 +114,11 @@ class _Rope(ctypes.Structure):
                 ("max_pos", ctypes.c_int32), ("axes", ctypes.c_int32)]
 
 
+class _StateBatch(ctypes.Structure):
+    _fields_ = [("begin", ctypes.c_void_p), ("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("seqs", ctypes.c_int32), ("max_q", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -122,7 +133,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     p, i, sz, st = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int
     l, f = ctypes.c_int64, ctypes.c_float
-    kc, kb = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
+    kc, kb, sb = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), ctypes.POINTER(_StateBatch)
     sig = {
         "tern_packed_code_bytes": (sz, [i, i]),
         "tern_scale_count": (sz, [i, i, i]),
@@ -159,6 +170,11 @@ def lib() -> ctypes.CDLL:
         "tern_kv_read": (st, [kc, kb, i, p, p, p]),
         "tern_kv_attn": (st, [kc, kb, i, p, l, i, f, i, i, p, p, sz, p]),
         "tern_kv_attn_workspace_bytes": (sz, [kc, kb, i, i, i, i]),
+        "tern_causal_conv": (st, [sb, i, p, i, l, i, i, p, p, i, i, p, i, p, l, p]),
+        "tern_scan": (st, [sb, i, i, i, i, i, p, l, p, l, p, l, p, i, l, p, i, p, p, p, i, p, p, sz, p]),
+        "tern_scan_workspace_bytes": (sz, [sb, i, i, i, i, i]),
+        "tern_rmsnorm_gated": (st, [p, i, l, p, i, l, p, i, i, i, f, i, i, p, p, i, p, l, p]),
+        "tern_rmsnorm_post": (st, [p, i, l, p, p, i, l, f, p, l, p, l, i, p, i, f, i, i, p, p, i, p, l, p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -918,3 +934,285 @@ def kv_attn(q, cache: KVCache, batch: KVBatch, scale: float, window: int = 0, si
     _check(lib().tern_kv_attn(cache._ref, batch._ref, tokens, q.data_ptr(), qs, heads, scale, window, sinks,
                               out.data_ptr(), wp, wb, _stream(stream)))
     return out
+
+
+# ------------------------------------------------------ recurrent block
+
+
+class StateBatch:
+    """The sequences of a call whose operators keep a state each: begin int32
+    [seqs + 1] (rows of the call's token matrices), src and dst int32 [seqs], the
+    slots of the state pools that hold a sequence's state before its rows (-1:
+    zeros) and take the one after them (-1: not kept); max_q bounds the rows of
+    a sequence. src and dst may agree; no slot that one sequence writes may be
+    another's. The arrays are read when the kernels run, so a captured graph
+    follows their updates."""
+
+    def __init__(self, begin, src, dst, max_q: int):
+        torch = _torch()
+        _dev(src, torch.int32, "src")
+        if src.dim() != 1:
+            raise ValueError(f"src must be [seqs], got {tuple(src.shape)}")
+        seqs = src.shape[0]
+        _dev(dst, torch.int32, "dst", (seqs,), src.device)
+        _dev(begin, torch.int32, "begin", (seqs + 1,), src.device)
+        _int32(max_q, "max_q")
+        self.begin, self.src, self.dst = begin, src, dst
+        self.seqs, self.max_q, self.device = seqs, int(max_q), src.device
+        self._struct = _StateBatch(begin.data_ptr(), src.data_ptr(), dst.data_ptr(), seqs, self.max_q)
+        self._ref = ctypes.byref(self._struct)
+        self._workspace = {}  # sizes of a call -> workspace bytes
+
+
+def _on_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _whole(t, name, shape, device):
+    """Checks a contiguous float32 or bfloat16 tensor; returns its type."""
+    kind, _ = _rows(t, name, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return kind
+
+
+def _bf16_rows(t, name, shape, device):
+    kind, stride = _rows(t, name, shape, device)
+    if kind != 1:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    return stride
+
+
+_ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def causal_conv(x, weight, state, batch: StateBatch, bias=None, activation="silu", out=None, stream=None):
+    """out [rows, channels] bf16: the causal convolution of x [rows, channels]
+    (float32 or bfloat16, rows may lie apart) with weight [channels, width] and
+    bias [channels] along every sequence, then `activation` ("silu" or None).
+    state [slots, width - 1, channels], of x's type: the last inputs of each slot's
+    sequence, oldest first, read and updated as the batch says. Rows that no
+    sequence has, or one that the call leaves out (see tern_state_batch in
+    tern.h), are not written: they hold what out held, or memory's contents."""
+    device = _on_gpu(x, "x")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [rows, channels], got {tuple(shape)}")
+    rows, channels = shape
+    xt, xs = _rows(x, "x", shape, device)
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [channels, width], got {tuple(weight.shape)}")
+    width = weight.shape[1]
+    wt = _whole(weight, "weight", (channels, width), device)
+    bp = None
+    if bias is not None:
+        if _whole(bias, "bias", (channels,), device) != wt:
+            raise TypeError("bias must have the weight's type")
+        bp = bias.data_ptr()
+    if state.dim() != 3:
+        raise ValueError(f"state must be [slots, width - 1, channels], got {tuple(state.shape)}")
+    slots = state.shape[0]
+    if _whole(state, "state", (slots, width - 1, channels), device) != xt:
+        raise TypeError("state must have the type of x")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}; expected one of {tuple(_ACTIVATIONS)}")
+    _on_device(batch, "batch", device)
+    ys = channels
+    if out is None:
+        out = _empty(shape, _torch().bfloat16, device, stream)
+    else:
+        ys = _bf16_rows(out, "out", shape, device)
+    _check(lib().tern_causal_conv(batch._ref, rows, x.data_ptr(), xt, xs, channels, width, weight.data_ptr(), bp, wt,
+                                  _ACTIVATIONS[activation], state.data_ptr(), slots, out.data_ptr(), ys, _stream(stream)))
+    return out
+
+
+def scan_workspace_bytes(batch: StateBatch, rows: int, heads: int, dim: int, groups: int, state_dim: int) -> int:
+    sizes = (rows, heads, dim, groups, state_dim)
+    n = batch._workspace.get(sizes)
+    if n is None:
+        for name, x in zip(("rows", "heads", "dim", "groups", "state_dim"), sizes):
+            _int32(x, name)
+        n = lib().tern_scan_workspace_bytes(batch._ref, *sizes)
+        if n == ctypes.c_size_t(-1).value:
+            raise TernError(2, lib().tern_last_error().decode())
+        batch._workspace[sizes] = n
+    return n
+
+
+def scan_workspace(batch: StateBatch, rows: int, heads: int, dim: int, groups: int, state_dim: int, stream=None):
+    """A workspace for scan calls of these sizes (None if they need none), for a
+    caller that keeps one from call to call."""
+    n = scan_workspace_bytes(batch, rows, heads, dim, groups, state_dim)
+    return None if n == 0 else _empty((n,), _torch().uint8, batch.device, stream)
+
+
+def scan(x, b, c, dt, a, state, batch: StateBatch, d=None, dt_bias=None, softplus=True, out=None, workspace=None,
+         stream=None):
+    """out [rows, heads, dim] bf16: the selective state space scan of x [rows,
+    heads, dim] with b and c [rows, groups, state_dim] (bfloat16, rows may lie
+    apart, as in a convolution's output), steps dt [rows, heads] (float32 or
+    bfloat16, rows may lie apart; plus dt_bias [heads], through softplus), decay
+    rates a [heads] and the skip d [heads], all float32. state float32 [slots,
+    heads, state_dim, dim] is read and updated as the batch says. Rows that no
+    sequence has, or one that the call leaves out (see tern_state_batch in
+    tern.h), are not written: they hold what out held, or memory's contents."""
+    device = _on_gpu(x, "x")
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must be [rows, heads, dim], got {tuple(shape)}")
+    rows, heads, dim = shape
+    xs = _bf16_rows(x, "x", shape, device)
+    if b.dim() != 3:
+        raise ValueError(f"b must be [rows, groups, state_dim], got {tuple(b.shape)}")
+    groups, n = b.shape[1:]
+    bs = _bf16_rows(b, "b", (rows, groups, n), device)
+    cs = _bf16_rows(c, "c", (rows, groups, n), device)
+    dtt, dts = _rows(dt, "dt", (rows, heads), device)
+    f32 = _torch().float32
+    _dev(a, f32, "a", (heads,), device)
+    if d is not None:
+        _dev(d, f32, "d", (heads,), device)
+    if dt_bias is not None:
+        _dev(dt_bias, f32, "dt_bias", (heads,), device)
+    if state.dim() != 4:
+        raise ValueError(f"state must be [slots, heads, state_dim, dim], got {tuple(state.shape)}")
+    slots = state.shape[0]
+    _dev(state, f32, "state", (slots, heads, n, dim), device)
+    _on_device(batch, "batch", device)
+    if out is None:
+        out = _empty(shape, x.dtype, device, stream)
+    else:
+        _dev(out, x.dtype, "out", shape, device)
+    if workspace is None:
+        workspace = scan_workspace(batch, rows, heads, dim, groups, n, stream)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of x")
+    wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check(lib().tern_scan(batch._ref, rows, heads, dim, groups, n, x.data_ptr(), xs, b.data_ptr(), bs, c.data_ptr(), cs,
+                           dt.data_ptr(), dtt, dts, None if dt_bias is None else dt_bias.data_ptr(), int(softplus),
+                           a.data_ptr(), None if d is None else d.data_ptr(), state.data_ptr(), slots, out.data_ptr(),
+                           wp, wb, _stream(stream)))
+    return out
+
+
+def _norm_outputs(shape, device, q, scale, y, made):
+    """Pointers of a norm's outputs (q, scale, y, stride of y); `made`: they are
+    this module's own, of the right shape."""
+    T, K = shape
+    qp = sp = yp = None
+    ys = 0
+    if y is not None:
+        ys = K if made else _bf16_rows(y, "y", shape, device)
+        yp = y.data_ptr()
+    if q is not None:
+        if not made:
+            _dev(q, _torch().int8, "q", (T, K), device)
+            _dev(scale, _torch().float32, "scale", (T,), device)
+        qp, sp = q.data_ptr(), scale.data_ptr()
+    return qp, sp, yp, ys
+
+
+def _matrix(x):
+    device, shape = _on_gpu(x, "x"), x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, K], got {tuple(shape)}")
+    return device, shape
+
+
+def _gated(x, z, weight, eps, group, gate_first, q, scale, layout, y, stream, made):
+    device, shape = _matrix(x)
+    T, K = shape
+    xt, xs = _rows(x, "x", shape, device)
+    zt, zs = _rows(z, "z", shape, device)
+    wt = _whole(weight, "weight", shape[1:], device)
+    qp, sp, yp, ys = _norm_outputs(shape, device, q, scale, y, made)
+    _check(lib().tern_rmsnorm_gated(x.data_ptr(), xt, xs, z.data_ptr(), zt, zs, weight.data_ptr(), wt,
+                                    K if group is None else group, int(gate_first), eps, T, K, qp, sp, Q_LAYOUTS[layout],
+                                    yp, ys, _stream(stream)))
+
+
+def rmsnorm_gated(x, z, weight, eps=1e-6, group=None, gate_first=True, y=None, stream=None):
+    """y [T, K] bf16 = the RMS norm over groups of `group` channels (default: the
+    row) of x silu(z), times weight, or with gate_first=False that of x, times
+    weight and silu(z). x and z: float32 or bfloat16, rows may lie apart."""
+    made = y is None
+    if made:
+        y = _empty(x.shape, _torch().bfloat16, x.device, stream)
+    _gated(x, z, weight, eps, group, gate_first, None, None, "row_major", y, stream, made)
+    return y
+
+
+def rmsnorm_gated_s8(x, z, weight, eps=1e-6, group=None, gate_first=True, q=None, scale=None, y=None,
+                     layout="row_major", stream=None):
+    """rmsnorm_gated with an 8-bit output: (q int8 [T, K] in `layout`, scale
+    float32 [T]), as linear_s8_q takes them; `y` (bf16) is written too when given."""
+    made = q is None and scale is None and y is None
+    if q is None:
+        q = _empty(x.shape, _torch().int8, x.device, stream)
+    if scale is None:
+        scale = _empty(x.shape[:1], _torch().float32, x.device, stream)
+    _gated(x, z, weight, eps, group, gate_first, q, scale, layout, y, stream, made)
+    return q, scale
+
+
+def _post(x, post_weight, residual, weight, eps, alpha, gate, residual_out, q, scale, layout, y, stream, made):
+    device, shape = _matrix(x)
+    T, K = shape
+    xt, xs = _rows(x, "x", shape, device)
+    wt = _whole(post_weight, "post_weight", shape[1:], device)
+    wp = gp = None
+    gt = gs = 0
+    if weight is not None:
+        if _whole(weight, "weight", shape[1:], device) != wt:
+            raise TypeError("weight must have the post_weight's type")
+        wp = weight.data_ptr()
+    if gate is not None:
+        if gate.dim() == 1:
+            gt = _whole(gate, "gate", shape[1:], device)
+        else:
+            gt, gs = _rows(gate, "gate", shape, device)
+        gp = gate.data_ptr()
+    rt, rs = _rows(residual, "residual", shape, device)
+    op, os_ = residual.data_ptr(), rs
+    if residual_out is not None and residual_out is not residual:
+        ot, os_ = _rows(residual_out, "residual_out", shape, device)
+        if ot != rt:
+            raise TypeError("residual_out must have the residual's type")
+        op = residual_out.data_ptr()
+    qp, sp, yp, ys = _norm_outputs(shape, device, q, scale, y, made)
+    _check(lib().tern_rmsnorm_post(x.data_ptr(), xt, xs, post_weight.data_ptr(), gp, gt, gs, alpha, residual.data_ptr(), rs,
+                                   op, os_, rt, wp, wt, eps, T, K, qp, sp, Q_LAYOUTS[layout], yp, ys, _stream(stream)))
+
+
+def rmsnorm_post(x, post_weight, residual, weight=None, eps=1e-6, scale=1.0, gate=None, residual_out=None, y=None,
+                 stream=None):
+    """The norm behind a block: h = residual + scale gate norm(x) post_weight,
+    written to residual_out (default: the residual itself) in the residual's type,
+    and y [T, K] bf16 = norm(h) weight, the next block's input (None without a
+    weight). gate: [K] or [T, K] (None: 1). Activations: float32 or bfloat16, rows
+    may lie apart."""
+    if weight is None:
+        if y is not None:
+            raise ValueError("y without a weight")
+        _post(x, post_weight, residual, None, eps, scale, gate, residual_out, None, None, "row_major", None, stream, True)
+        return None
+    made = y is None
+    if made:
+        y = _empty(x.shape, _torch().bfloat16, x.device, stream)
+    _post(x, post_weight, residual, weight, eps, scale, gate, residual_out, None, None, "row_major", y, stream, made)
+    return y
+
+
+def rmsnorm_post_s8(x, post_weight, residual, weight, eps=1e-6, scale=1.0, gate=None, residual_out=None, q=None,
+                    act_scale=None, y=None, layout="row_major", stream=None):
+    """rmsnorm_post with an 8-bit output: (q int8 [T, K] in `layout`, act_scale
+    float32 [T]), as linear_s8_q takes them; `y` (bf16) is written too when given."""
+    made = q is None and act_scale is None and y is None
+    if q is None:
+        q = _empty(x.shape, _torch().int8, x.device, stream)
+    if act_scale is None:
+        act_scale = _empty(x.shape[:1], _torch().float32, x.device, stream)
+    _post(x, post_weight, residual, weight, eps, scale, gate, residual_out, q, act_scale, layout, y, stream, made)
+    return q, act_scale

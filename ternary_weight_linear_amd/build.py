@@ -67,6 +67,9 @@ UNITS = [
     ("tern_norm.hip", []),
     ("tern_cache.hip", []),
     ("tern_attn.hip", S8_FLAGS),
+    ("tern_conv.hip", []),
+    ("tern_scan.hip", S8_FLAGS),
+    ("tern_gatednorm.hip", []),
 ]
 
 

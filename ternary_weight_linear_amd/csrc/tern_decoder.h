@@ -3,6 +3,7 @@
 #pragma once
 #include <type_traits>
 
+#include "tern.h"
 #include "tern_device.h"
 
 namespace tern {
@@ -63,6 +64,21 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const bf16x2 v = {(__bf16)lo, (__bf16)hi};
   return __builtin_bit_cast(uint32_t, v);
+}
+
+// 8 consecutive elements as fp32.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&o)[8]) {
+  if constexpr (TYPE == TERN_F32) {
+    const f32x4* f = (const f32x4*)((const float*)p + at);
+    const f32x4 a = f[0], b = f[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = a[i], o[4 + i] = b[i];
+  } else {
+    const u32x4 w = *(const u32x4*)((const uint16_t*)p + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[2 * i] = bf16_lo(w[i]), o[2 * i + 1] = bf16_hi(w[i]);
+  }
 }
 
 // Sum over the 64 lanes, the same in every lane and in a fixed order: a

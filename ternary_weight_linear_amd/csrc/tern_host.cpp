@@ -54,8 +54,9 @@ const char* const kKernelNames[TERN_KERNEL_COUNT] = {
     "smallt_tile",     "smallt_tile_reduce", "b16_prefill",   "s8_mma",           "s8_reduce",
     "s8_row",          "s8_acc_export",     "stream_read",    "gemv_t5",          "chain",
     "smallt_narrow",   "rmsnorm",           "kv_append",      "kv_read",          "kv_attn",
-    "kv_attn_tile",    "kv_attn_join"};
-static_assert(TERN_KERNEL_COUNT == 27, "one name per kernel id");
+    "kv_attn_tile",    "kv_attn_join",      "causal_conv",    "scan_step",        "rmsnorm_gated",
+    "rmsnorm_post"};
+static_assert(TERN_KERNEL_COUNT == 31, "one name per kernel id");
 
 // ------------------------------------------------------------ configuration
 
@@ -1476,6 +1477,7 @@ tern_status tern_debug_s8_acc(const int8_t* q, int T, const tern_weights* W, int
 }
 
 #include "tern_host_decoder.h"
+#include "tern_host_recurrent.h"
 
 void tern_probe_snapshot(uint64_t out[TERN_RUNG_COUNT]) {
   for (int i = 0; i < TERN_RUNG_COUNT; ++i) out[i] = g_probe[i].load(std::memory_order_relaxed);

@@ -279,4 +279,65 @@ constexpr int kKvMaxRuns = 256;    // per head
 constexpr int kKvMaxUnits = 2048;  // with runs: their prefix sums are in LDS
 TERN_WEAK int launch_kv_attn(const KvAttnArgs& a, const KvAttnPlan& p, void* ws, void* stream);
 
+// ---- the recurrent block's operators (tern_conv.hip, tern_scan.hip, tern_gatednorm.hip).
+
+struct StateBatch {
+  const int32_t* begin;
+  const int32_t* src;
+  const int32_t* dst;
+  int seqs, max_q, rows;  // rows of the call
+};
+
+struct ConvArgs {
+  StateBatch batch;
+  const void* x;
+  const void* w;
+  const void* bias;  // or nullptr
+  void* state;       // of x's type
+  uint16_t* y;
+  int64_t x_stride, y_stride;
+  int type, w_type, channels, width, slots;
+  bool silu;
+};
+TERN_WEAK int64_t conv_blocks(const ConvArgs& a);
+TERN_WEAK int launch_conv(const ConvArgs& a, void* stream);
+
+struct ScanArgs {
+  StateBatch batch;
+  const uint16_t *x, *b, *c;  // bf16
+  const void* dt;
+  const float *dt_bias, *a, *d;  // dt_bias and d may be nullptr
+  float* state;
+  uint16_t* y;
+  int64_t x_stride, b_stride, c_stride, dt_stride;
+  int heads, dim, groups, state_dim, dt_type, slots;
+  bool softplus;
+};
+TERN_WEAK int launch_scan_step(const ScanArgs& a, void* stream);
+
+struct GatedNormArgs {
+  const void *x, *z, *w;
+  int8_t* q;         // or nullptr
+  float* act_scale;  // with q
+  uint16_t* y;       // or nullptr
+  int64_t x_stride, z_stride, y_stride;
+  int x_type, z_type, w_type, T, K, group;
+  float eps;
+  bool gate_first, operand_order;
+};
+TERN_WEAK int launch_rmsnorm_gated(const GatedNormArgs& a, void* stream);
+
+struct PostNormArgs {
+  const void *x, *post_w, *gate, *r, *w;  // gate and w may be nullptr
+  void* r_out;
+  int8_t* q;
+  float* act_scale;
+  uint16_t* y;
+  int64_t x_stride, gate_stride, r_stride, r_out_stride, y_stride;
+  int x_type, gate_type, r_type, w_type, T, K;
+  float scale, eps;
+  bool operand_order;
+};
+TERN_WEAK int launch_rmsnorm_post(const PostNormArgs& a, void* stream);
+
 }  // namespace tern

@@ -25,22 +25,6 @@ namespace tern {
 namespace {
 using namespace dev;
 
-// 8 consecutive elements as fp32.
-template <int TYPE>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&o)[8]) {
-  if constexpr (TYPE == TERN_F32) {
-    const f32x4* f = (const f32x4*)((const float*)p + at);
-    const f32x4 a = f[0], b = f[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = a[i], o[4 + i] = b[i];
-  } else {
-    const u32x4 w = *(const u32x4*)((const uint16_t*)p + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[2 * i] = bf16_lo(w[i]), o[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-
-
 // One workgroup per token; each thread owns up to NU chunks of 16 elements in
 // two runs of 8: 32 apart, which makes 16 consecutive bytes of q in operand
 // order, or next to each other where K is no multiple of 64. The layout of q

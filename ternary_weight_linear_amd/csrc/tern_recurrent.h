@@ -1,0 +1,45 @@
+// tern_recurrent.h -- device-side helpers of the recurrent block's kernels
+// (convolution, scan, gated norm). Internal, not installed.
+#pragma once
+#include "tern_decoder.h"
+#include "tern_internal.h"
+
+namespace tern {
+namespace dev {
+
+// exp(x) to about 2 ulp: the rounding of x log2(e), which the hardware's 2^t
+// alone would multiply by |x|, is put back to first order. Results below
+// 2^-126 are 0, above fp32 infinite; NaN stays NaN.
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr float kHi = 0x1.715476p+0f, kLo = 0x1.4ae0cp-26f;  // log2(e) = kHi + kLo
+  const float y = x < -150.f ? -150.f : x > 88.72f ? 88.72f : x;
+  const float t = y * kHi;
+  const float r = __builtin_fmaf(y, kLo, __builtin_fmaf(y, kHi, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float v = __builtin_fmaf(e, r * 0.693147182f, e);
+  return x > 88.7228317f ? __builtin_inff() : v;
+}
+
+// z / (1 + exp(-z)). From -88 down it is 0 where the exact value is below 2^-120.
+__device__ __forceinline__ float silu(float z) {
+  const float e = exp_of(z < -88.7f ? 88.7f : -z);
+  return z * __builtin_amdgcn_rcpf(1.f + e);
+}
+
+// log(1 + exp(v)).
+__device__ __forceinline__ float softplus(float v) { return (v > 0.f ? v : 0.f) + log1pf(exp_of(-fabsf(v))); }
+
+// Rows of sequence s in the call, [row, row + n): n is 0 for one that is left
+// out. What comes from device memory is bounded here.
+struct Rows {
+  int64_t row;
+  int n;
+};
+__device__ __forceinline__ Rows rows_of(const StateBatch& b, int s) {
+  const int q0 = b.begin[s], q1 = b.begin[s + 1];
+  if (q0 < 0 || q1 < q0 || q1 > b.rows || q1 - q0 > b.max_q) return Rows{0, 0};
+  return Rows{q0, q1 - q0};
+}
+
+}  // namespace dev
+}  // namespace tern
