@@ -629,12 +629,13 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
  * recurrence is stable. state: fp32 [slots][heads][state_dim][dim]; y: bf16
  * [rows][heads][dim].
  * dim is 32, 64 or 128, state_dim 64, 128 or 256. x, b, c, their rows, state and y
- * are 16-byte aligned. y overlaps no input.
- * States are fp32 throughout. Calls with more than 16 rows a sequence work in
- * blocks of 64 rows through matrix products of bf16 operands with fp32 sums: B, C
- * and x enter as they are, weighted x and the state as sums of two bf16 numbers (16
- * bits), the weights inside a block likewise. There, a value that is not finite
- * makes the results that depend on it infinite or NaN; no other rows or channels.
+ * are 16-byte aligned, their rows at most 2^22 elements apart. y overlaps no input.
+ * States are fp32 throughout. Calls with max_q of more than 8 rows work in
+ * blocks of 32 rows through matrix products of bf16 operands with fp32 sums: B, C
+ * and x enter as they are, weighted x enters the next state with all of its 24
+ * bits; the weights inside a block and, for y only, the state before it are rounded
+ * to bf16. There, a value that is not finite makes the results that depend on it
+ * infinite or NaN; no other rows or channels.
  * ws: device, tern_scan_workspace_bytes() bytes for the same arguments (16-byte
  * aligned, any contents; NULL if 0); calls that share it must not overlap.
  * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.
@@ -730,6 +731,10 @@ typedef enum {
   TERN_KERNEL_KV_ATTN_JOIN,       /* tern_kv_attn: joins the runs of a split key axis */
   TERN_KERNEL_CAUSAL_CONV,        /* tern_causal_conv */
   TERN_KERNEL_SCAN_STEP,          /* tern_scan: token by token, the state in registers */
+  TERN_KERNEL_SCAN_PREPARE,       /* tern_scan: prompts, what does not depend on a state */
+  TERN_KERNEL_SCAN_STATES,        /* tern_scan: states of the segments of prompts */
+  TERN_KERNEL_SCAN_JOIN,          /* tern_scan: states at the starts of segments */
+  TERN_KERNEL_SCAN_BLOCKS,        /* tern_scan: prompts, blocks of 32 rows */
   TERN_KERNEL_RMSNORM_GATED,      /* tern_rmsnorm_gated */
   TERN_KERNEL_RMSNORM_POST,       /* tern_rmsnorm_post */
   TERN_KERNEL_COUNT

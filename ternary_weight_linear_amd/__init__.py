@@ -59,7 +59,8 @@ KERNELS = ("quant_s8", "quant_s8_row", "quant_s8_rot", "gemv_limb", "gemv_bf16",
            "smallt_wave", "smallt_tile", "smallt_tile_reduce", "b16_prefill", "s8_mma",
            "s8_reduce", "s8_row", "s8_acc_export", "stream_read", "gemv_t5", "chain",
            "smallt_narrow", "rmsnorm", "kv_append", "kv_read", "kv_attn", "kv_attn_tile",
-           "kv_attn_join", "causal_conv", "scan_step", "rmsnorm_gated", "rmsnorm_post")
+           "kv_attn_join", "causal_conv", "scan_step", "scan_prepare", "scan_states", "scan_join", "scan_blocks",
+           "rmsnorm_gated", "rmsnorm_post")
 
 # Symbols declared in include/tern.h (checked by the host tests).
 EXPORTS = ("tern_packed_code_bytes", "tern_scale_count", "tern_pack", "tern_unpack",

@@ -68,7 +68,8 @@ UNITS = [
     ("tern_cache.hip", []),
     ("tern_attn.hip", S8_FLAGS),
     ("tern_conv.hip", []),
-    ("tern_scan.hip", S8_FLAGS),
+    ("tern_scan.hip", []),
+    ("tern_scanblocks.hip", S8_FLAGS),
     ("tern_gatednorm.hip", []),
 ]
 

@@ -54,9 +54,9 @@ const char* const kKernelNames[TERN_KERNEL_COUNT] = {
     "smallt_tile",     "smallt_tile_reduce", "b16_prefill",   "s8_mma",           "s8_reduce",
     "s8_row",          "s8_acc_export",     "stream_read",    "gemv_t5",          "chain",
     "smallt_narrow",   "rmsnorm",           "kv_append",      "kv_read",          "kv_attn",
-    "kv_attn_tile",    "kv_attn_join",      "causal_conv",    "scan_step",        "rmsnorm_gated",
-    "rmsnorm_post"};
-static_assert(TERN_KERNEL_COUNT == 31, "one name per kernel id");
+    "kv_attn_tile",    "kv_attn_join",      "causal_conv",    "scan_step",        "scan_prepare",
+    "scan_states",     "scan_join",         "scan_blocks",    "rmsnorm_gated",    "rmsnorm_post"};
+static_assert(TERN_KERNEL_COUNT == 35, "one name per kernel id");
 
 // ------------------------------------------------------------ configuration
 

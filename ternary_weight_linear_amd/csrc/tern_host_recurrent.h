@@ -62,8 +62,44 @@ tern_status check_scan(const tern_state_batch* batch, int rows, int heads, int d
   if (groups < 1 || heads % groups != 0)
     return fail(TERN_ERR_SHAPE, "groups=%d must divide heads=%d", groups, heads);
   a->heads = heads, a->dim = dim, a->groups = groups, a->state_dim = state_dim, a->slots = slots;
-  if ((int64_t)batch->seqs * heads > kMaxGrid) return fail(TERN_ERR_SHAPE, "seqs * heads too large for one launch");
+  // a workgroup for every head, or for every 64 columns; segments are cut only where workgroups are few
+  if (2 * (int64_t)batch->seqs * heads > kMaxGrid || tern::scan_prepare_blocks(*a) > kMaxGrid)
+    return fail(TERN_ERR_SHAPE, "tern_scan: seqs * heads or seqs * max_q * groups too large for one launch");
   return TERN_OK;
+}
+
+constexpr int64_t kScanMaxStride = 1 << 22;  // elements: 64 rows stay below 2^30 bytes
+
+// Up to so many rows a sequence go token by token. Measured, token by token and in
+// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 49 and 52 us, with 12 rows 57 and 52; 64
+// sequences 150 and 156, 171 and 158; 2 of 40 heads of 128 x 256 with 12 rows 26 and 24.
+constexpr int kScanStepRows = 8;
+
+// Segments of a prompt: as many as make the launches shortest, in microseconds as
+// measured. A block of 32 tokens takes a workgroup 1.05 us in the last launch and
+// 0.75 us in the one before it, which only S > 1 segments need, while a compute
+// unit has one, and that much longer the more it has; two launches more cost 15 us. Measured, in all
+// (64 blocks, 160 units): 87, 111, 95, 100 and 105 us for 1, 2, 3, 4 and 6
+// segments; 256 blocks of 20 units: 261, 123, 74, 63, 59 and 64 us for 1, 4, 8, 11, 22 and 32.
+tern::ScanPlan plan_scan(const tern::ScanArgs& a) {
+  const int64_t blocks = (a.batch.max_q + tern::kScanBlock - 1) / tern::kScanBlock, units = tern::scan_units(a);
+  tern::ScanPlan p{1, (int)blocks * tern::kScanBlock};
+  double least = 0;
+  for (int64_t s = 1; s <= std::min<int64_t>(64, blocks / 4 + 1) && (s == 1 || units < kComputeUnits); ++s) {
+    const int64_t length = (blocks + s - 1) / s, used = (blocks + length - 1) / length;
+    const double each = 1.05 * std::max(1.0, (double)(units * used) / kComputeUnits);
+    const double before = used == 1 ? 0 : 0.75 * std::max(1.0, 1.1 * (double)(units * (used - 1)) / kComputeUnits);
+    const double us = length * (each + before) + (used == 1 ? 0 : 15);
+    if (s == 1 || us < least) {
+      least = us;
+      p.length = (int)length * tern::kScanBlock, p.segments = (int)used;
+    }
+  }
+  return p;
+}
+
+size_t scan_ws(const tern::ScanArgs& a) {
+  return a.batch.max_q <= kScanStepRows ? 0 : (size_t)tern::scan_ws_bytes(a, plan_scan(a));
 }
 
 }  // namespace
@@ -73,7 +109,7 @@ size_t tern_scan_workspace_bytes(const tern_state_batch* batch, int rows, int he
   tern::ScanArgs a{};
   if (check_scan(batch, rows, heads, dim, groups, state_dim, 1, &a)) return (size_t)-1;
   g_last_error.clear();
-  return 0;
+  return scan_ws(a);
 }
 
 tern_status tern_scan(const tern_state_batch* batch, int rows, int heads, int dim, int groups, int state_dim,
@@ -91,21 +127,24 @@ tern_status tern_scan(const tern_state_batch* batch, int rows, int heads, int di
   const int64_t shared = (int64_t)groups * state_dim;
   if (x_stride < (int64_t)heads * dim || b_stride < shared || c_stride < shared || dt_stride < heads)
     return fail(TERN_ERR_SHAPE, "tern_scan: a row stride is smaller than the row");
+  if (x_stride > kScanMaxStride || b_stride > kScanMaxStride || c_stride > kScanMaxStride)
+    return fail(TERN_ERR_SHAPE, "tern_scan: a row stride of x, b or c is larger than 2^22");
   if (!aligned16(x_bf16) || !aligned16(b_bf16) || !aligned16(c_bf16) || !aligned16(state) || !aligned16(y_bf16) ||
       x_stride % 8 != 0 || b_stride % 8 != 0 || c_stride % 8 != 0)
     return fail(TERN_ERR_ALIGN, "tern_scan: x, b, c, their rows, state and y must be 16-byte aligned");
   if (!aligned(dt, type_bytes(dt_type)) || !aligned(dt_bias, 4) || !aligned(a_decay, 4) || !aligned(d, 4))
     return fail(TERN_ERR_ALIGN, "tern_scan: dt, dt_bias, a and d must be aligned to their elements");
-  const size_t need = 0;
+  const size_t need = scan_ws(a);
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_ERR_WORKSPACE, "tern_scan needs %zu bytes of workspace, got %zu", need, ws ? ws_bytes : (size_t)0);
   if (need && !aligned16(ws)) return fail(TERN_ERR_ALIGN, "the workspace must be 16-byte aligned");
-  if (!tern::launch_scan_step) return no_unit();
+  if (!tern::launch_scan_step || !tern::launch_scan_blocks) return no_unit();
   a.x = (const uint16_t*)x_bf16, a.b = (const uint16_t*)b_bf16, a.c = (const uint16_t*)c_bf16, a.dt = dt;
   a.dt_bias = dt_bias, a.a = a_decay, a.d = d, a.state = state, a.y = (uint16_t*)y_bf16;
   a.x_stride = x_stride, a.b_stride = b_stride, a.c_stride = c_stride, a.dt_stride = dt_stride;
   a.dt_type = dt_type, a.softplus = softplus != 0;
-  const int err = tern::launch_scan_step(a, stream);
+  const int err = a.batch.max_q <= kScanStepRows ? tern::launch_scan_step(a, stream)
+                                                 : tern::launch_scan_blocks(a, plan_scan(a), ws, stream);
   if (err) return hip_fail(err, "scan launch");
   return call_ok();
 }

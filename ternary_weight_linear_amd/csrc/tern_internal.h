@@ -315,6 +315,29 @@ struct ScanArgs {
 };
 TERN_WEAK int launch_scan_step(const ScanArgs& a, void* stream);
 
+// Prompts (tern_scanblocks.hip): a sequence's tokens in `segments` pieces of
+// `length` (a multiple of 32), each walked by one workgroup for every 64
+// columns of a group's heads, a unit.
+struct ScanPlan {
+  int segments, length;
+};
+constexpr int kScanBlock = 32;
+constexpr int kScanHeadBytes = 2048 + 2 * kScanBlock * 4;  // prepared for a head and block
+inline int64_t scan_units(const ScanArgs& a) {
+  return ((int64_t)a.heads / a.groups * a.dim + 63) / 64 * a.groups * a.batch.seqs;
+}
+inline int64_t scan_prepare_blocks(const ScanArgs& a) {
+  return (int64_t)a.groups * a.batch.seqs * ((a.batch.max_q + kScanBlock - 1) / kScanBlock);
+}
+// Workspace: what is prepared for the blocks, then the segments' states and decays.
+inline int64_t scan_prepared_bytes(const ScanArgs& a) {
+  return ((int64_t)a.batch.rows / kScanBlock + a.batch.seqs + 1) * a.heads * kScanHeadBytes;
+}
+inline int64_t scan_ws_bytes(const ScanArgs& a, const ScanPlan& p) {
+  return scan_prepared_bytes(a) + scan_units(a) * (p.segments - 1) * 4 * ((int64_t)a.state_dim * 16 + 1) * 4;
+}
+TERN_WEAK int launch_scan_blocks(const ScanArgs& a, const ScanPlan& p, void* ws, void* stream);
+
 struct GatedNormArgs {
   const void *x, *z, *w;
   int8_t* q;         // or nullptr

@@ -26,8 +26,13 @@ __device__ __forceinline__ float silu(float z) {
   return z * __builtin_amdgcn_rcpf(1.f + e);
 }
 
-// log(1 + exp(v)).
-__device__ __forceinline__ float softplus(float v) { return (v > 0.f ? v : 0.f) + log1pf(exp_of(-fabsf(v))); }
+// log(1 + exp(v)): with u = exp(-|v|) and w = 1 + u as rounded, log(1 + u) is
+// log(w) and what the rounding took, over w.
+__device__ __forceinline__ float softplus(float v) {
+  const float u = exp_of(-fabsf(v)), w = 1.f + u;
+  const float rest = (u - (w - 1.f)) * __builtin_amdgcn_rcpf(w);
+  return (v > 0.f ? v : 0.f) + __builtin_fmaf(__builtin_amdgcn_logf(w), 0.693147182f, rest);
+}
 
 // Rows of sequence s in the call, [row, row + n): n is 0 for one that is left
 // out. What comes from device memory is bounded here.

@@ -63,16 +63,16 @@ class Scan:
         self.N = state.shape[1]
 
     # Token by token: the recurrence's errors, and for y a sum of N + 1 terms
-    # (N / 4 products one after the other, then a tree). In blocks: operands as
-    # pairs of bf16 numbers keep 16 bits (2^-17 each, two of them in a term), sums of
-    # up to N + 64 products.
+    # (N / 4 products one after the other, then a tree). In blocks: sums of up to N +
+    # 64 products; a term of y has one factor rounded to bf16 (of the block's weights or
+    # of the state before it), off by at most 2^-8 of itself. The state's terms keep 24 bits.
     def y_bound(self, blocks):
-        e = self.rel[..., None] + (self.N + 8) * U + (2.0 ** -15 + 64 * U if blocks else 0)
+        e = self.rel[..., None] + (self.N + 8) * U + (2.0 ** -8 + 64 * U if blocks else 0)
         return e * self.ymag
 
     def s_bound(self, blocks):
         e = (self.rel[-1] if len(self.rel) else np.zeros(self.s.shape[0]))[:, None, None]
-        return (e + (2.0 ** -16 + 64 * U if blocks else 0)) * self.smag
+        return (e + (64 * U if blocks else 0)) * self.smag
 
 
 def gated(x, z, w, eps, group, first):

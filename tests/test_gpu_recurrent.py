@@ -177,7 +177,7 @@ class ScanCase:
             if n == 0 or i in left_out:
                 continue
             r = self.reference(i)
-            blocks = max(self.lens) > 16
+            blocks = max(self.lens) > 8
             near(y[self.begin[i]:self.begin[i + 1]], r.y, r.y_bound(blocks), i)
             if 0 <= self.dst[i] < len(self.pool):
                 got = state[self.dst[i]]
@@ -195,7 +195,7 @@ def run_scan(torch, tl, c, **kw):
 
 @pytest.mark.parametrize("p", [32, 64, 128])
 @pytest.mark.parametrize("n", [64, 128, 256])
-@pytest.mark.parametrize("lens,heads,groups", [([1], 3, 1), ([4, 1, 0, 3], 4, 2), ([16, 9], 2, 2)])
+@pytest.mark.parametrize("lens,heads,groups", [([1], 3, 1), ([4, 1, 0, 3], 4, 2), ([8, 5], 2, 2)])
 def test_scan_steps(torch, tl, p, n, lens, heads, groups):
     c = ScanCase(torch, p + n, lens, heads, groups, p, n)
     y, state = run_scan(torch, tl, c)
@@ -203,7 +203,7 @@ def test_scan_steps(torch, tl, p, n, lens, heads, groups):
     c.check(host(y), host(state))
 
 
-SCAN_LENS = [[17], [63, 64, 65], [1, 130, 0, 200], [509, 18]]
+SCAN_LENS = [[9], [17], [31, 32, 33], [63, 64, 65], [1, 130, 0, 200], [509, 18]]
 
 
 @pytest.mark.parametrize("lens", SCAN_LENS)
@@ -294,7 +294,7 @@ def test_scan_forgets_at_a_large_step(torch, tl):
     y, state = (host(v) for v in run_scan(torch, tl, c))
     r = ref.Scan(c.x[t + 1:], c.b[t + 1:], c.c[t + 1:], c.dt[t + 1:, :2], c.a.astype(np.float64), np.zeros_like(c.pool[0]),
                  c.d.astype(np.float64), None, False)
-    # inside a run of 16 rows exponents are differences of sums up to 16 * 150: 2400 * 2^-24 and a few roundings each
+    # inside a block of 32 rows exponents are differences of sums up to 32 * 216 log(2): 4790 * 2^-24 and a few roundings each
     e = r.y_bound(True) + 2.0 ** -11 * r.ymag
     near(y[t + 1:], r.y, e)
     assert (np.abs(state[c.dst[0]] - r.s) <= r.s_bound(True) + 2.0 ** -11 * r.smag).all()

@@ -77,6 +77,7 @@ def test_conv_refuses_grids_that_one_launch_cannot_hold(tl):
     (NULL, dict(state=None)), (NULL, dict(y=None)), (VALUE, dict(dtt=2)), (VALUE, dict(y=P)), (SHAPE, dict(rows=0)),
     (SHAPE, dict(heads=0)), (SHAPE, dict(heads=65536)), (SHAPE, dict(groups=0)), (SHAPE, dict(groups=3)),
     (SHAPE, dict(dim=48)), (SHAPE, dict(n=32)), (SHAPE, dict(xs=255)), (SHAPE, dict(bs=255)), (SHAPE, dict(cs=0)),
+    (SHAPE, dict(xs=(1 << 22) + 8)), (SHAPE, dict(bs=(1 << 22) + 8)), (SHAPE, dict(cs=(1 << 22) + 8)),
     (SHAPE, dict(dts=3)), (SHAPE, dict(slots=0)), (ALIGN, dict(x=P + 8)), (ALIGN, dict(b=P + 8)), (ALIGN, dict(cs=260)),
     (ALIGN, dict(state=P + 4)), (ALIGN, dict(y=2 * P + 2)), (ALIGN, dict(dt=P + 2)), (ALIGN, dict(bias=P + 2)),
     (ALIGN, dict(a=P + 1)), (ALIGN, dict(d=P + 2))])
