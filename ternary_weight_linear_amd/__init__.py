@@ -978,6 +978,16 @@ def _whole(t, name, shape, device):
     return kind
 
 
+def _f32(t, name, shape, device):
+    """_dev for float32, without its steps where all is well."""
+    try:
+        if t.dtype is _torch().float32 and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _dev(t, _torch().float32, name, shape, device)
+
+
 def _bf16_rows(t, name, shape, device):
     kind, stride = _rows(t, name, shape, device)
     if kind != 1:
@@ -1068,19 +1078,21 @@ def scan(x, b, c, dt, a, state, batch: StateBatch, d=None, dt_bias=None, softplu
     if b.dim() != 3:
         raise ValueError(f"b must be [rows, groups, state_dim], got {tuple(b.shape)}")
     groups, n = b.shape[1:]
-    bs = _bf16_rows(b, "b", (rows, groups, n), device)
-    cs = _bf16_rows(c, "c", (rows, groups, n), device)
+    shared = (rows, groups, n)
+    bs = _bf16_rows(b, "b", shared, device)
+    cs = _bf16_rows(c, "c", shared, device)
     dtt, dts = _rows(dt, "dt", (rows, heads), device)
-    f32 = _torch().float32
-    _dev(a, f32, "a", (heads,), device)
+    each = (heads,)
+    dp = bp = None
+    _f32(a, "a", each, device)
     if d is not None:
-        _dev(d, f32, "d", (heads,), device)
+        _f32(d, "d", each, device)
+        dp = d.data_ptr()
     if dt_bias is not None:
-        _dev(dt_bias, f32, "dt_bias", (heads,), device)
-    if state.dim() != 4:
-        raise ValueError(f"state must be [slots, heads, state_dim, dim], got {tuple(state.shape)}")
-    slots = state.shape[0]
-    _dev(state, f32, "state", (slots, heads, n, dim), device)
+        _f32(dt_bias, "dt_bias", each, device)
+        bp = dt_bias.data_ptr()
+    slots = state.shape[0] if state.dim() == 4 else -1
+    _f32(state, "state", (slots, heads, n, dim), device)
     _on_device(batch, "batch", device)
     if out is None:
         out = _empty(shape, x.dtype, device, stream)
@@ -1092,9 +1104,8 @@ def scan(x, b, c, dt, a, state, batch: StateBatch, d=None, dt_bias=None, softplu
         raise ValueError("workspace must be a contiguous tensor on the device of x")
     wp, wb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _check(lib().tern_scan(batch._ref, rows, heads, dim, groups, n, x.data_ptr(), xs, b.data_ptr(), bs, c.data_ptr(), cs,
-                           dt.data_ptr(), dtt, dts, None if dt_bias is None else dt_bias.data_ptr(), int(softplus),
-                           a.data_ptr(), None if d is None else d.data_ptr(), state.data_ptr(), slots, out.data_ptr(),
-                           wp, wb, _stream(stream)))
+                           dt.data_ptr(), dtt, dts, bp, int(softplus), a.data_ptr(), dp, state.data_ptr(), slots,
+                           out.data_ptr(), wp, wb, _stream(stream)))
     return out
 
 

@@ -54,59 +54,47 @@ template <int TYPE, int W>
 __global__ void __launch_bounds__(256) tern_causal_conv_kernel(ConvArgs a) {
   constexpr int CH = kChannels<TYPE>, BYTES = 16 / CH;
   const int s = blockIdx.y;
-  const Rows r = rows_of(a.batch, s);
   const int blocks = a.channels / CH;
   const int at = blockIdx.x * 256 + threadIdx.x;
   const int run = at / blocks, c0 = (at - run * blocks) * CH;
   const int t0 = run * kRun;
-  if (t0 >= r.n) return;
-  const char* x = (const char*)a.x + (r.row * a.x_stride + c0) * BYTES;
-  const int64_t step = a.x_stride * BYTES;
-  const int64_t slot = (int64_t)(W - 1) * a.channels;  // elements
-  float past[W - 1][CH];
-  if (run == 0) {
-    u32x4 old[W - 1];
-    const int src = a.batch.src[s], dst = a.batch.dst[s];
-    const bool has = src >= 0 && src < a.slots;
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-      old[j] = u32x4{0, 0, 0, 0};
-      if (has) old[j] = *(const u32x4*)((const char*)a.state + (src * slot + (int64_t)j * a.channels + c0) * BYTES);
-      widen<TYPE>(old[j], past[j]);
-    }
-    if (dst >= 0 && dst < a.slots) {
-      // new state j: input n - (W - 1) + j of this call, or from the old state before it
-      u32x4 now[W - 1];
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) {
-        const int i = r.n - (W - 1) + j;
-        now[j] = old[W - 2];
-#pragma unroll
-        for (int o = 0; o < W - 1; ++o)
-          if (i == o - (W - 1)) now[j] = old[o];
-        if (i >= 0) now[j] = *(const u32x4*)(x + i * step);
-      }
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-        *(u32x4*)((char*)a.state + (dst * slot + (int64_t)j * a.channels + c0) * BYTES) = now[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) widen<TYPE>(*(const u32x4*)(x + (t0 - (W - 1) + j) * step), past[j]);
-  }
+  // What does not depend on the batch's arrays is asked for before them: a single
+  // token waits for two trips to memory, one for the arrays and one for the rest.
   float w[CH * W], bias[CH];
   load_weights(a.w, (int64_t)c0 * W, a.w_type, w);
 #pragma unroll
   for (int i = 0; i < CH; ++i) bias[i] = 0.f;
   if (a.bias) load_weights(a.bias, c0, a.w_type, bias);
+  const int src = a.batch.src[s], dst = a.batch.dst[s];
+  const Rows r = rows_of(a.batch, s);
+  if (t0 >= r.n) return;
+  const char* x = (const char*)a.x + (r.row * a.x_stride + c0) * BYTES;
+  const int64_t step = a.x_stride * BYTES;
   const int last = min(t0 + kRun, r.n);
-  uint16_t* y = a.y + r.row * a.y_stride + c0;
-  for (int t = t0; t < last; t += kStep) {
-    u32x4 raw[kStep];
+  u32x4 raw[kStep], old[W - 1];
 #pragma unroll
-    for (int j = 0; j < kStep; ++j) raw[j] = *(const u32x4*)(x + min(t + j, last - 1) * step);
+  for (int j = 0; j < kStep; ++j)
+    if (t0 + j < last) raw[j] = *(const u32x4*)(x + (t0 + j) * step);
+  const int64_t slot = (int64_t)(W - 1) * a.channels;  // elements
+  if (run > 0) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) old[j] = *(const u32x4*)(x + (t0 - (W - 1) + j) * step);
+  } else {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      old[j] = u32x4{0, 0, 0, 0};
+      if (src >= 0 && src < a.slots)
+        old[j] = *(const u32x4*)((const char*)a.state + (src * slot + (int64_t)j * a.channels + c0) * BYTES);
+    }
+  }
+  float past[W - 1][CH];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) widen<TYPE>(old[j], past[j]);
+  uint16_t* y = a.y + r.row * a.y_stride + c0;
+  for (int t = t0;;) {
 #pragma unroll
     for (int j = 0; j < kStep; ++j) {
+      if (t + j >= last) break;
       float now[CH], o[CH];
       widen<TYPE>(raw[j], now);
 #pragma unroll
@@ -120,16 +108,34 @@ __global__ void __launch_bounds__(256) tern_causal_conv_kernel(ConvArgs a) {
         for (int k = 0; k + 1 < W - 1; ++k) past[k][i] = past[k + 1][i];
         past[W - 2][i] = now[i];
       }
-      if (t + j < last) {
-        uint32_t out[CH / 2];
+      uint32_t out[CH / 2];
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) out[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
-        if constexpr (CH == 4)
-          *(uint2*)(y + (t + j) * a.y_stride) = uint2{out[0], out[1]};
-        else
-          *(u32x4*)(y + (t + j) * a.y_stride) = u32x4{out[0], out[1], out[2], out[3]};
-      }
+      for (int i = 0; i < CH / 2; ++i) out[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+      if constexpr (CH == 4)
+        *(uint2*)(y + (t + j) * a.y_stride) = uint2{out[0], out[1]};
+      else
+        *(u32x4*)(y + (t + j) * a.y_stride) = u32x4{out[0], out[1], out[2], out[3]};
     }
+    if ((t += kStep) >= last) break;
+#pragma unroll
+    for (int j = 0; j < kStep; ++j)
+      if (t + j < last) raw[j] = *(const u32x4*)(x + (t + j) * step);
+  }
+  if (run == 0 && dst >= 0 && dst < a.slots) {
+    // new state j: input n - (W - 1) + j of this call, or from the old state before it
+    u32x4 now[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      const int i = r.n - (W - 1) + j;
+      now[j] = old[W - 2];
+#pragma unroll
+      for (int o = 0; o < W - 1; ++o)
+        if (i == o - (W - 1)) now[j] = old[o];
+      if (i >= 0) now[j] = *(const u32x4*)(x + i * step);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      *(u32x4*)((char*)a.state + (dst * slot + (int64_t)j * a.channels + c0) * BYTES) = now[j];
   }
 }
 

@@ -20,10 +20,10 @@ __device__ __forceinline__ float exp_of(float x) {
   return x > 88.7228317f ? __builtin_inff() : v;
 }
 
-// z / (1 + exp(-z)). From -88 down it is 0 where the exact value is below 2^-120.
+// z / (1 + exp(-z)), to about 6 + 1.5 |z| roundings (the exponent's is not put
+// back: the results are rounded to 8 bits); 0 from -88 down, where it is below 2^-120.
 __device__ __forceinline__ float silu(float z) {
-  const float e = exp_of(z < -88.7f ? 88.7f : -z);
-  return z * __builtin_amdgcn_rcpf(1.f + e);
+  return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f));
 }
 
 // log(1 + exp(v)): with u = exp(-|v|) and w = 1 + u as rounded, log(1 + u) is

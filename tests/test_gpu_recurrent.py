@@ -343,7 +343,7 @@ def test_gated_norm(torch, tl, T, K, group, xt, zt, wt, first):
     step = np.abs(want).max(1) / 127
     assert (np.abs(host(s) - step) <= (ref.GATED + 2 * U) * step + 2.0 ** -100).all()
     q, s = host(q).astype(np.float64), host(s).astype(np.float64)
-    # the quotient is within 127 * 2 * 64 ulp of the exact one, the code half a step from it
+    # the quotient is within 127 * 2 * GATED of the exact one, the code half a step from it
     live = step > 0
     assert (np.abs(q[live] - want[live] / step[live, None]) <= 0.5 + 127 * (2 * ref.GATED + 4 * U)).all()
     assert (q[~live] == 0).all() and (s[~live] == 0).all()
