@@ -326,8 +326,10 @@ constexpr int kScanHeadBytes = 2048 + 2 * kScanBlock * 4;  // prepared for a hea
 inline int64_t scan_units(const ScanArgs& a) {
   return ((int64_t)a.heads / a.groups * a.dim + 63) / 64 * a.groups * a.batch.seqs;
 }
+constexpr int kScanPrepareHeads = 8;  // a workgroup of the first launch
 inline int64_t scan_prepare_blocks(const ScanArgs& a) {
-  return (int64_t)a.groups * a.batch.seqs * ((a.batch.max_q + kScanBlock - 1) / kScanBlock);
+  const int64_t heads = a.heads / a.groups;
+  return (heads + kScanPrepareHeads - 1) / kScanPrepareHeads * a.groups * a.batch.seqs * ((a.batch.max_q + kScanBlock - 1) / kScanBlock);
 }
 // Workspace: what is prepared for the blocks, then the segments' states and decays.
 inline int64_t scan_prepared_bytes(const ScanArgs& a) {

@@ -101,22 +101,33 @@ static_assert(kHeadBytes == 2048 + 2 * kBlock * 4, "layout of a head's block");
 // begin + 32 i, so row / 32 + s differs for all of them.
 __device__ __forceinline__ int64_t block_at(int64_t row, int s) { return (row >> 5) + s; }
 
-// M and factors: a workgroup takes a block of a sequence and a group. Its first
-// waves make C B^T once, then every wave takes two heads at a time. Bound by
-// the latency of its chain and by writing M, 2 KB a head and block.
+// M and factors: a workgroup takes a block of a sequence and eight heads of a
+// group, two a wave. Its first three waves make C B^T, 16 x 16 blocks each. Bound
+// by the chain of loads, sums and products of each workgroup, then by writing M, 2 KB a
+// head and block.
 template <int N>
 __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint8_t* ws) {
   __shared__ __attribute__((aligned(16))) f32x4 blocks[3][64];
   __shared__ __attribute__((aligned(16))) float shared[4][2][2][kBlock];  // L and D of a wave's heads
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, low = lane & 31, half = lane >> 5;
   const int low16 = lane & 15, quarter = lane >> 4;
-  const int hpg = a.heads / a.groups, count = (a.batch.max_q + kBlock - 1) / kBlock;
-  const int g = blockIdx.x % a.groups, s = blockIdx.x / a.groups / count;
-  const int t0 = (blockIdx.x / a.groups - s * count) * kBlock;
+  const int hpg = a.heads / a.groups, parts = (hpg + kScanPrepareHeads - 1) / kScanPrepareHeads;
+  const int count = (a.batch.max_q + kBlock - 1) / kBlock;
+  int at = blockIdx.x;
+  const int h0 = at % parts * kScanPrepareHeads + 2 * wave;  // of the group
+  at /= parts;
+  const int g = at % a.groups;
+  at /= a.groups;
+  const int s = at / count, t0 = (at - s * count) * kBlock;
   const Rows rows = rows_of(a.batch, s);
   if (t0 >= rows.n) return;
   const int last = min(rows.n - t0, kBlock);
   const int64_t row0 = rows.row + t0;
+  // a token a lane, a head each half
+  const int h = g * hpg + min(h0 + half, hpg - 1);
+  const int64_t step = (row0 + min(low, last - 1)) * a.dt_stride + h;
+  float D = a.dt_type == TERN_F32 ? ((const float*)a.dt)[step] : __uint_as_float((uint32_t)((const uint16_t*)a.dt)[step] << 16);
+  const float rate = a.a[h] * kLog2e, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   // C B^T of the block, transposed, in 16 x 16 blocks (t, s): (0, 0), (0, 1), (1, 1)
   if (wave < 3) {
     const uint16_t* b = a.b + (row0 + min(wave == 2 ? 16 + low16 : low16, last - 1)) * a.b_stride + g * N + 8 * quarter;
@@ -129,55 +140,42 @@ __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint
     for (int q = 0; q < N / 32; ++q) cb = mfma(bf[q], cf[q], cb);
     blocks[wave][lane] = cb;
   }
-  bool first = true;
-  f32x4 cb[3];
-  for (int h0 = 2 * wave; h0 < hpg || first; h0 += 8) {
-    // D, L: a token a lane, a head each half
-    const int h = g * hpg + min(h0 + half, hpg - 1);
-    const int64_t at = (row0 + min(low, last - 1)) * a.dt_stride + h;
-    float D = a.dt_type == TERN_F32 ? ((const float*)a.dt)[at] : __uint_as_float((uint32_t)((const uint16_t*)a.dt)[at] << 16);
-    if (a.dt_bias) D += a.dt_bias[h];
-    if (a.softplus) D = softplus(D);
-    float e = D * (a.a[h] * kLog2e);
-    e = e < -216.f ? -216.f : e;  // 2^-216 is 0 in fp32; a longer sum would only lose bits of the others
-    if (low >= last) D = 0.f, e = 0.f;
-    const float L = sums_up(e, lane), R = sums_down(e, lane);
-    const float next = moved<0x130>(R);  // wave_shl: the next lane's, the sum behind the token
-    const float behind = low == 31 ? 0.f : next;
-    shared[wave][half][0][low] = L, shared[wave][half][1][low] = D;
-    if (h0 + half < hpg) {
-      float* to = (float*)(ws + (block_at(row0, s) * a.heads + h) * kHeadBytes + 2048) + low;
-      to[0] = __builtin_amdgcn_exp2f(L), to[kBlock] = D * __builtin_amdgcn_exp2f(behind);
-    }
-    if (first) {
-      __syncthreads();
+  D += bias;
+  if (a.softplus) D = softplus(D);
+  float e = D * rate;
+  e = e < -216.f ? -216.f : e;  // 2^-216 is 0 in fp32; a longer sum would only lose bits of the others
+  if (low >= last) D = 0.f, e = 0.f;
+  const float L = sums_up(e, lane), R = sums_down(e, lane);
+  const float next = moved<0x130>(R);  // wave_shl: the next lane's, the sum behind the token
+  const float behind = low == 31 ? 0.f : next;
+  shared[wave][half][0][low] = L, shared[wave][half][1][low] = D;
+  if (h0 + half < hpg) {
+    float* to = (float*)(ws + (block_at(row0, s) * a.heads + h) * kHeadBytes + 2048) + low;
+    to[0] = __builtin_amdgcn_exp2f(L), to[kBlock] = D * __builtin_amdgcn_exp2f(behind);
+  }
+  __syncthreads();
+  const int over = low16 - 4 * quarter;  // s - t + k in the blocks on the diagonal
 #pragma unroll
-      for (int j = 0; j < 3; ++j) cb[j] = blocks[j][lane];
-      first = false;
-    }
-    const int over = low16 - 4 * quarter;  // s - t + k in the blocks on the diagonal
+  for (int i = 0; i < 2; ++i) {
+    if (h0 + i >= hpg) break;
+    const float(&Ls)[kBlock] = shared[wave][i][0];
+    const float(&Ds)[kBlock] = shared[wave][i][1];
+    const float own[2] = {Ls[low16], Ls[16 + low16]};
+    uint2 out[3];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (h0 + i >= hpg) break;
-      const float(&Ls)[kBlock] = shared[wave][i][0];
-      const float(&Ds)[kBlock] = shared[wave][i][1];
-      const float own[2] = {Ls[low16], Ls[16 + low16]};
-      uint2 out[3];
+    for (int j = 0; j < 3; ++j) {
+      const int t = j == 2 ? 16 : 0;
+      const f32x4 cb = blocks[j][lane], ft = *(const f32x4*)&Ls[t + 4 * quarter], fd = *(const f32x4*)&Ds[t + 4 * quarter];
+      float m[4];
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int t = j == 2 ? 16 : 0;
-        const f32x4 ft = *(const f32x4*)&Ls[t + 4 * quarter], fd = *(const f32x4*)&Ds[t + 4 * quarter];
-        float m[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m[k] = cb[j][k] * (__builtin_amdgcn_exp2f(own[j > 0] - ft[k]) * fd[k]);
-          if (j != 1) m[k] = over < k ? 0.f : m[k];
-        }
-        out[j] = uint2{pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3])};
+      for (int k = 0; k < 4; ++k) {
+        m[k] = cb[k] * (__builtin_amdgcn_exp2f(own[j > 0] - ft[k]) * fd[k]);
+        if (j != 1) m[k] = over < k ? 0.f : m[k];
       }
-      u32x4* to = (u32x4*)(ws + (block_at(row0, s) * a.heads + g * hpg + h0 + i) * kHeadBytes) + lane;
-      to[0] = u32x4{out[0].x, out[0].y, 0, 0}, to[64] = u32x4{out[1].x, out[1].y, out[2].x, out[2].y};
+      out[j] = uint2{pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3])};
     }
+    u32x4* to = (u32x4*)(ws + (block_at(row0, s) * a.heads + g * hpg + h0 + i) * kHeadBytes) + lane;
+    to[0] = u32x4{out[0].x, out[0].y, 0, 0}, to[64] = u32x4{out[1].x, out[1].y, out[2].x, out[2].y};
   }
 }
 
