@@ -20,10 +20,14 @@ __device__ __forceinline__ float exp_of(float x) {
   return x > 88.7228317f ? __builtin_inff() : v;
 }
 
-// z / (1 + exp(-z)), to about 6 + 1.5 |z| roundings (the exponent's is not put
-// back: the results are rounded to 8 bits); 0 from -88 down, where it is below 2^-120.
+// z / (1 + exp(-z)), to about 6 + |z| / 4 roundings: the rounding of the exponent
+// -z log2(e) is put back to first order, that of the constant is not. 0 from -88
+// down, where the value is below 2^-120.
 __device__ __forceinline__ float silu(float z) {
-  return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+  constexpr float kLog2e = -0x1.715476p+0f;
+  const float c = __builtin_amdgcn_fmed3f(z, -126.f, 126.f), t = c * kLog2e;
+  const float e = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(__builtin_fmaf(c, kLog2e, -t), 0.693147182f, 1.f);
+  return z * __builtin_amdgcn_rcpf(1.f + e);
 }
 
 // log(1 + exp(v)): with u = exp(-|v|) and w = 1 + u as rounded, log(1 + u) is

@@ -24,9 +24,9 @@ def conv(x, w, bias, act, past):
     # at most `width` products and sums after the bias, each rounded once
     e = k * U * (sum(np.abs(t) for t in terms) + (0 if bias is None else np.abs(bias)))
     if act:
-        # |d silu / dz| < 1.1; the exponent z log2(e) rounded (twice: the constant too), the
-        # exponential (2 ulp), sum, reciprocal (1 ulp), product
-        y, e = silu(y), 1.1 * e + (8 + 2 * np.abs(y)) * U * np.abs(silu(y)) + 2.0 ** -120
+        # |d silu / dz| < 1.1; log2(e) rounded, the exponential (2 ulp) and its correction,
+        # sum, reciprocal (1 ulp), product
+        y, e = silu(y), 1.1 * e + (8 + np.abs(y)) * U * np.abs(silu(y)) + 2.0 ** -120
     return y, rows[rows.shape[0] - (k - 1):], e
 
 
@@ -87,10 +87,10 @@ def gated(x, z, w, eps, group, first):
     return v if first else v * g
 
 
-# The gated norm's relative error for |z| < 12: the gate 8 + 2 |z|, four products; the
+# The gated norm's relative error for |z| < 12: the gate 8 + |z|, four products; the
 # sum of squares twice that of the operands and up to 16 + 32 + 6 sums one after the
 # other, halved by the root; root, quotient.
-GATED = 108 * U
+GATED = 84 * U
 
 
 def post(x, pw, r, scale, gate, eps):
