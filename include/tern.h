@@ -635,7 +635,8 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
  * and x enter as they are, weighted x enters the next state with all of its 24
  * bits; the weights inside a block and, for y only, the state before it are rounded
  * to bf16. There, a value that is not finite makes the results that depend on it
- * infinite or NaN; no other rows or channels.
+ * infinite or NaN; no other rows or channels. A block takes exp() of D a summed over up to
+ * 32 rows, so a state that grows (D a > 0) leaves fp32 where that sum passes 88.
  * ws: device, tern_scan_workspace_bytes() bytes for the same arguments (16-byte
  * aligned, any contents; NULL if 0); calls that share it must not overlap.
  * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.

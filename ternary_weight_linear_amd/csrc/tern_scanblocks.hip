@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint
   }
 }
 
-// Where the state of segment j of a unit lies, for wave 0 of it: states in the order
-// of the registers, [NB][lane] times four, behind them one decay a wave.
+// Where the state at the start of segment j of a unit lies, for strip 0 of it: states in
+// the order of the registers, [N / 16][lane] times four, behind them one decay a strip,
+// that of the segment before.
 __device__ __forceinline__ int64_t state_at(int unit, int units, int j) { return ((int64_t)j * units + unit) * 4; }
 
 template <int P, int N, bool STATES>
@@ -297,8 +298,10 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   const int64_t slot = (int64_t)a.heads * N * P;
   constexpr int64_t kWave = N * 16;
   if constexpr (!STATES) {
-    if (seg > 0) {
-      const f32x4* p = (const f32x4*)(ws + (state_at(unit, units, seg - 1) + strip) * kWave) + upper * NB * 64 + lane;
+    // The first segment's too, if there are others: the slot may be the one that the last of
+    // them writes in this launch.
+    if (!(seg == 0 && ends)) {
+      const f32x4* p = (const f32x4*)(ws + (state_at(unit, units, seg) + strip) * kWave) + upper * NB * 64 + lane;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) S[nb] = p[nb * 64];
     } else {
@@ -459,11 +462,11 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   }
   if constexpr (!STATES) store_y(t0 - kBlock, turn);
   if constexpr (STATES) {
-    const int64_t to = state_at(unit, units, seg) + strip;
+    const int64_t to = state_at(unit, units, seg + 1) + strip;
     f32x4* p = (f32x4*)(ws + to * kWave) + upper * NB * 64 + lane;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) p[nb * 64] = S[nb];
-    if (lane == 0 && !upper) ws[state_at(0, units, plan.segments - 1) * kWave + to] = decay;
+    if (lane == 0 && !upper) ws[state_at(0, units, plan.segments) * kWave + to] = decay;
   } else {
     const int dst = a.batch.dst[s];
     if (ends && live && dst >= 0 && dst < a.slots) {
@@ -476,9 +479,9 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   }
 }
 
-// Turns the segments' own states into the states behind them: state j becomes
-// decay_j (the one before it) + state j, from the sequence's state on. A thread
-// takes four elements of a wave's state through all segments, whose loads go out
+// Turns the segments' own states into the states at the segments' starts: state 0 is
+// the sequence's, state j becomes decay_j (the one before it) + state j. A thread
+// takes four elements of a strip's state through all segments, whose loads go out
 // eight at a time.
 template <int P, int N>
 __global__ void __launch_bounds__(256) tern_scan_join_kernel(ScanArgs a, ScanPlan plan, float* ws) {
@@ -502,20 +505,21 @@ __global__ void __launch_bounds__(256) tern_scan_join_kernel(ScanArgs a, ScanPla
 #pragma unroll
     for (int r = 0; r < 4; ++r) S[r] = p[r * P];
   }
-  const float* decays = ws + state_at(0, units, plan.segments - 1) * kWave;
+  const float* decays = ws + state_at(0, units, plan.segments) * kWave;
   f32x4* at = (f32x4*)(ws + (state_at(unit, units, 0) + wave) * kWave) + nb * 64 + lane;
   const int64_t step = (int64_t)units * kWave;  // of four floats: a segment
-  for (int j0 = 0; j0 < count; j0 += AT_ONCE) {
+  at[0] = S;
+  for (int j0 = 1; j0 <= count; j0 += AT_ONCE) {
     f32x4 v[AT_ONCE];
     float decay[AT_ONCE];
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
-      const int j = min(j0 + i, count - 1);
+      const int j = min(j0 + i, count);
       v[i] = at[j * step], decay[i] = decays[state_at(unit, units, j) + wave];
     }
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
-      if (j0 + i >= count) break;
+      if (j0 + i > count) break;
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(decay[i], S[r], v[i][r]);
       at[(j0 + i) * step] = S;

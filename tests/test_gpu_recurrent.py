@@ -214,7 +214,58 @@ SCAN_LENS = [[9], [17], [31, 32, 33], [63, 64, 65], [1, 130, 0, 200], [509, 18]]
 def test_scan_prompts(torch, tl, lens, p, n, heads, groups, kw):
     c = ScanCase(torch, p * n + sum(lens), lens, heads, groups, p, n, **kw)
     y, state = run_scan(torch, tl, c)
+    assert tl.last_kernels() == ["scan_prepare", "scan_blocks"]
     c.check(host(y), host(state))
+
+
+SEGMENTS = ["scan_blocks", "scan_join", "scan_prepare", "scan_states"]
+
+
+@pytest.mark.parametrize("p,n,heads,groups,lens,place", [
+    (64, 128, 2, 1, [2500, 0, 31, 700], "apart"), (32, 64, 5, 1, [1, 2049], "apart"), (128, 256, 1, 1, [1536], "in place"),
+    (64, 64, 4, 2, [1601, 1600], "in place"), (32, 256, 2, 2, [1300, 1400], "from zeros"), (128, 64, 1, 1, [33, 4100], "in place")])
+def test_scan_in_segments(torch, tl, p, n, heads, groups, lens, place):
+    """Few heads and long prompts, which several workgroups share: each starts from its segment's state."""
+    c = ScanCase(torch, p + n + heads, lens, heads, groups, p, n, slots=2 * len(lens) + 1)
+    if place == "in place":
+        c.dst = list(c.src)
+    elif place == "from zeros":
+        c.src[0], c.dst[1] = -1, -1
+    y, state = run_scan(torch, tl, c)
+    assert sorted(tl.last_kernels()) == SEGMENTS
+    c.check(host(y), host(state))
+
+
+def test_captured_segments(torch, tl):
+    """A captured scan in segments, in place and replayed with other lengths, gives what eager calls give."""
+    n = 1800
+    c = ScanCase(torch, 18, [n, n], 2, 1, 64, 128)
+    t, state = c.tensors(torch), dev(torch, c.pool)
+    begin, slots = (torch.tensor(v, dtype=torch.int32, device="cuda:0") for v in (c.begin, c.src))
+    batch = tl.StateBatch(begin, slots, slots, max_q=n)
+    work = tl.scan_workspace(batch, 2 * n, 2, 64, 1, 128)
+    out = torch.zeros((2 * n, 2, 64), dtype=torch.bfloat16, device="cuda:0")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        tl.scan(state=state, batch=batch, workspace=work, out=out, **t)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tl.scan(state=state, batch=batch, workspace=work, out=out, **t)
+    assert sorted(tl.last_kernels()) == SEGMENTS
+    for first, second in ((n, n), (1, n), (97, 0), (1000, 800)):
+        begin.copy_(torch.tensor([0, first, first + second], dtype=torch.int32))
+        state.copy_(dev(torch, c.pool)), out.zero_()
+        work.fill_(255)  # any contents: NaN
+        graph.replay()
+        torch.cuda.synchronize()
+        kept, mine = state.clone(), out.clone()
+        state.copy_(dev(torch, c.pool)), out.zero_()
+        tl.scan(state=state, batch=batch, out=out, **t)
+        assert torch.equal(kept, state) and torch.equal(mine, out), (first, second)
+        assert torch.isfinite(out).all() and (out[first + second:] == 0).all()
+        assert torch.isfinite(state).all()
 
 
 def test_scan_from_zeros_in_place_and_not_kept(torch, tl):

@@ -92,6 +92,20 @@ def test_scan_refuses_too_many_heads_for_a_launch(tl):
     assert b"too large" in tl.lib().tern_last_error()
 
 
+def test_scan_asks_for_its_workspace(tl):
+    size = tl.lib().tern_scan_workspace_bytes
+    assert size(batch(tl, max_q=8), 6, 4, 64, 2, 128) == 0
+    for b, rows in ((batch(tl, max_q=9), 18), (batch(tl, seqs=1, max_q=5000), 5000)):
+        need = size(b, rows, 4, 64, 2, 128)
+        assert 0 < need < 1 << 30
+        kw = dict(rows=rows, ws=P, wb=need)
+        assert scan(tl, b, **{**kw, "ws": None}) == WORKSPACE
+        assert scan(tl, b, **{**kw, "wb": need - 1}) == WORKSPACE
+        assert scan(tl, b, **{**kw, "ws": P + 8}) == ALIGN
+    # segments of a long prompt of few heads hold a state each
+    assert size(batch(tl, seqs=1, max_q=5000), 5000, 4, 64, 2, 128) - size(batch(tl, seqs=1, max_q=32), 5000, 4, 64, 2, 128) >= 2 * 4 * 4 * 64 * 128
+
+
 def gated(tl, **kw):
     a = dict(x=P, xt=1, xs=256, z=P, zt=0, zs=256, w=P, wt=0, group=64, first=1, eps=1e-6, T=3, k=256, q=P, s=P, layout=1,
              y=P, ys=256)
