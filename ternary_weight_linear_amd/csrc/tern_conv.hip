@@ -8,6 +8,10 @@
 // registers, so a row is read once, and W - 1 rows twice at the runs' ends.
 // The thread of a sequence's first run reads the old state before it writes
 // the new one, and no other thread reads that slot.
+//
+// Measured (W = 4): 2048 tokens of 12288 channels, fp32, in 30.6 us, 4.9 TB/s, the rate of
+// a copy; runs of 8 tokens take 55 us, of 32 30.0. 32 single tokens, bf16, in 5.5 us, two
+// trips to memory and a launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -17,8 +21,8 @@ namespace tern {
 namespace {
 using namespace dev;
 
-constexpr int kRun = 16;   // tokens a thread
-constexpr int kStep = 8;   // rows asked for together
+constexpr int kRun = 16;  // tokens a thread
+constexpr int kStep = 8;  // rows asked for together
 
 template <int TYPE>
 constexpr int kChannels = TYPE == TERN_F32 ? 4 : 8;  // 16 bytes

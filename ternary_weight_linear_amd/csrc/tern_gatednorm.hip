@@ -5,6 +5,10 @@
 // Bound by HBM (7 bytes an element: bf16 x, fp32 z, int8 codes; 13 with fp32 x
 // and residual). One workgroup a token, 16 elements a thread as in the plain
 // norm, everything read once and kept in registers between the reductions.
+//
+// Measured: gated, 2048 x 10240 to codes in 34.4 us, 4.3 TB/s; 509 x 5120 in
+// groups of a head, 6.4 us. Behind a block, 2048 x 5120 to codes in 31.2 us, 4.4 TB/s; 17
+// tokens 5.1 us, three trips to memory and two reductions. Copies reach 5.0 TB/s.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

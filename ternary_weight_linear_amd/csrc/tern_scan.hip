@@ -1,4 +1,5 @@
-// tern_scan.hip -- gfx950 kernels of tern_scan: the selective state space scan.
+// tern_scan.hip -- gfx950 kernel of tern_scan for few rows a sequence: the
+// selective state space scan token by token.
 //
 //   S[t] = exp(D[t] a) S[t-1] + D[t] B[t] x[t]^T  (N x P),  y[t] = C[t] S[t] + d x[t].
 //
@@ -7,6 +8,11 @@
 // token. A workgroup takes one sequence and head; lane l of a wave holds 4 of
 // the P columns (16 bytes of a state row) of N / 4 / (256 / P) rows, so C S is summed in
 // the lane and crosses lanes once a token.
+//
+// Measured (160 heads of 64 x 128): one token of 32 sequences 65 us, 5.2 TB/s of
+// states read and written, as a copy; 4 tokens of 16 sequences 41 us, 4.2 TB/s (each
+// further token costs about 3 us, its reduction and barrier); one token of one sequence
+// 5.2 us, the launch and three trips to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
