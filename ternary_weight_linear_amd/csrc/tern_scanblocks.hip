@@ -331,11 +331,14 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   const int tr = 4 * quarter + (lane >> 2 & 3), piece = lane & 3;  // transposed: row, 4 columns
   const int xt = place<8>(tr, 2 * strip + (piece >> 1)) + (piece & 1) * 8;
   constexpr int BT = NB < 4 ? NB : 4, CO = KQ < 2 ? KQ : 2;
-  int bt[BT], co[CO];
+  int bt[BT], co[2][CO];  // C's rows that the wave ends, and the other wave's
 #pragma unroll
   for (int i = 0; i < BT; ++i) bt[i] = place<CH>(tr, 2 * (upper * NB + i) + (piece >> 1)) + (piece & 1) * 8;
 #pragma unroll
-  for (int i = 0; i < CO; ++i) co[i] = place<CH>(low, 4 * (upper * KQ + i) + quarter);
+  for (int i = 0; i < CO; ++i) {
+    co[0][i] = place<CH>(16 * upper + low, 4 * (upper * KQ + i) + quarter);
+    co[1][i] = place<CH>(16 - 16 * upper + low, 4 * (upper * KQ + i) + quarter);
+  }
 
   // y of a block leaves while the next one is worked on: the wave of each half of
   // the state ends 16 of its rows, with the other's part of them, and brings them through
@@ -347,9 +350,13 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   const float skip = a.d ? a.d[head] : 0.f;
   const int xown = place<8>(16 * upper + low, 2 * strip + (quarter >> 1)) + (quarter & 1) * 8;
   f32x4 out;
+  float scale;  // exp(L) of the lane's row
   auto store_y = [&](int t0, int turn) {  // of block t0
     const f32x4 other = parts[turn][wave ^ 4][lane];
-    *(uint2*)yput = uint2{pack_bf16(out[0] + other[0], out[1] + other[1]), pack_bf16(out[2] + other[2], out[3] + other[3])};
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(scale, other[r], out[r]);
+    *(uint2*)yput = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     const int n = min(last - t0, kBlock) - 1;
     const rsrc_t yres = make_rsrc(y + (int64_t)t0 * a.heads * P, live ? n * ystep + 2 * P : 0);
     typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -381,18 +388,13 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
           v[2 * j + 1] = pack_bf16(S[2 * q + j][2], S[2 * q + j][3]);
         }
 #pragma unroll
-        for (int sb = 0; sb < 2; ++sb)
-          acc[sb] = mfma(v, *(const u32x4*)(cs[turn] + co[q & 1] + (q >> 1) * 128 + 16 * sb * ROW), acc[sb]);
+        for (int j = 0; j < 2; ++j) acc[j] = mfma(v, *(const u32x4*)(cs[turn] + co[j][q & 1] + (q >> 1) * 128), acc[j]);
       }
-#pragma unroll
-      for (int sb = 0; sb < 2; ++sb) {
-        const float scale = fs[turn][wave][16 * sb + low];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[sb][r] *= scale;
-      }
-      parts[turn][wave][lane] = upper ? acc[0] : acc[1];
-      acc[0] = upper ? acc[1] : acc[0];
+      parts[turn][wave][lane] = acc[1];
+      scale = fs[turn][wave][16 * upper + low];
       const uint2 own = *(const uint2*)(xs[turn] + xown);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[0][r] *= scale;
       acc[0][0] = __builtin_fmaf(skip, bf16_lo(own.x), acc[0][0]), acc[0][1] = __builtin_fmaf(skip, bf16_hi(own.x), acc[0][1]);
       acc[0][2] = __builtin_fmaf(skip, bf16_lo(own.y), acc[0][2]), acc[0][3] = __builtin_fmaf(skip, bf16_hi(own.y), acc[0][3]);
       out = mfma(xf, mt, acc[0]);
