@@ -32,7 +32,7 @@
 // few workgroups cannot hide; the matrix cores and HBM are far from full. Measured:
 // 2048 tokens of 160 heads of 64 x 128 in 12 + 77 us (11 us of matrix products at the whole
 // chip's rate, 21 us of traffic); 3 x 509 of 40 heads of 128 x 64 in 5 + 19; 8192 of 20
-// heads of 64 x 128 in 11 segments, 8 + 21 + 6 + 34. Products of 32 x 32 x 16 with 128
+// heads of 64 x 128 in 11 segments, 8 + 21 + 6 + 33. Products of 32 x 32 x 16 with 128
 // columns a workgroup take 65 us against 82 here for 512 tokens of 1024 heads, and are
 // slower where units are few.
 #include <hip/hip_runtime.h>
