@@ -49,6 +49,17 @@ __device__ __forceinline__ float load_dt(const ScanArgs& a, int64_t row, int h) 
   return a.dt_type == TERN_F32 ? ((const float*)a.dt)[at] : __uint_as_float((uint32_t)((const uint16_t*)a.dt)[at] << 16);
 }
 
+// Sums over lanes 32 apart of a (in the lower lanes) and b (in the upper ones).
+__device__ __forceinline__ float halves(float a, float b) {
+  const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(v[0]) + __uint_as_float(v[1]);
+}
+// Sums over lanes 16 apart of a (in rows 0 and 2 of 16 lanes) and b (in rows 1 and 3).
+__device__ __forceinline__ float rows16(float a, float b) {
+  const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(v[0]) + __uint_as_float(v[1]);
+}
+
 template <int P, int N>
 __global__ void __launch_bounds__(256) tern_scan_step_kernel(ScanArgs a) {
   constexpr int LPR = P / 4, NG = 64 / LPR, R = N / 4 / NG;
@@ -74,6 +85,7 @@ __global__ void __launch_bounds__(256) tern_scan_step_kernel(ScanArgs a) {
   const uint16_t* x = a.x + r.row * a.x_stride + h * P + p4;
   const uint16_t* b = a.b + r.row * a.b_stride + g * N + n0;
   const uint16_t* c = a.c + r.row * a.c_stride + g * N + n0;
+  const int upper = lane >> 5, mine = (lane >> 4 & 1) * 2 + upper;  // columns that the lane ends
   const float decay = a.a[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, skip = a.d ? a.d[h] : 0.f;
   Raw<4> xt;
   Raw<R> bt, ct;
@@ -101,17 +113,18 @@ __global__ void __launch_bounds__(256) tern_scan_step_kernel(ScanArgs a) {
         y[i] = __builtin_fmaf(ck, st[k][i], y[i]);
       }
     }
+    if (a.d && threadIdx.x < LPR) {
 #pragma unroll
-    for (int m = LPR; m < 64; m *= 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += __shfl_xor(y[i], m);
+      for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(skip, xn.at(i), y[i]);
     }
-    if (lane < LPR) {
-      if (wave == 0 && a.d) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = __builtin_fmaf(skip, xn.at(i), y[i]);
-      }
-      *(f32x4*)&part[t & 1][wave][p4] = f32x4{y[0], y[1], y[2], y[3]};
+    // The lanes that hold the same columns add up, each ending one or two of the four.
+    float* to = part[t & 1][wave] + p4;
+    if constexpr (P == 128) {
+      to[upper] = halves(y[0], y[1]), to[2 + upper] = halves(y[2], y[3]);
+    } else {
+      float v = rows16(halves(y[0], y[1]), halves(y[2], y[3]));
+      if constexpr (P == 32) v += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), 0x128, 0xf, 0xf, true));  // row_ror:8
+      if (lane % 16 < LPR) to[mine] = v;
     }
     __syncthreads();  // the other half of `part` was read before the barrier of the token in between
     if (threadIdx.x < P / 2) {

@@ -366,6 +366,35 @@ def test_scan_in_pieces(torch, tl):
     assert (np.abs(host(state)[c.dst[0]] - want.s) <= want.s_bound(True)).all()
 
 
+@pytest.mark.parametrize("lens", [[3, 2], [40, 600]])
+def test_offsets_past_32_bits(torch, tl, lens):
+    """Slots behind 4 GiB of a pool and rows behind 4 GiB of x give the bits of small ones."""
+    c = ScanCase(torch, 19, lens, 160, 8, 64, 128)
+    t = c.tensors(torch)
+    near_state = dev(torch, c.pool)
+    y0 = tl.scan(state=near_state, batch=batch_of(torch, tl, c.begin, c.src, c.dst), **t)
+    slots, rows = 900, c.begin[-1]
+    far = torch.zeros((slots, 160, 128, 64), device="cuda:0")  # 4.7e9 bytes
+    src, dst = [slots - 1, slots - 2], [slots - 3, slots - 4]
+    for s, f in zip(c.src, src):
+        far[f] = dev(torch, c.pool[s])
+    step = 1 << 22  # the largest distance of rows: 640 of them pass 4 GiB
+    x = torch.zeros(step * rows, dtype=torch.bfloat16, device="cuda:0").as_strided((rows, 160, 64), (step, 64, 1))
+    t["x"] = x.copy_(t["x"])
+    y = tl.scan(state=far, batch=batch_of(torch, tl, c.begin, src, dst), **t)
+    assert torch.equal(y, y0)
+    for d, f in zip(c.dst, dst):
+        assert torch.equal(near_state[d], far[f])
+    ch, slots = 16384, 24000
+    z, w = torch.randn((rows, ch), device="cuda:0"), torch.randn((ch, 4), device="cuda:0")
+    past = torch.randn((4, 3, ch), device="cuda:0")
+    far = torch.zeros((slots, 3, ch), device="cuda:0")  # 4.7e9 bytes
+    far[slots - 1], far[slots - 2] = past[0], past[1]
+    o0 = tl.causal_conv(z, w, past, batch_of(torch, tl, c.begin, [0, 1], [2, 3]))
+    o = tl.causal_conv(z, w, far, batch_of(torch, tl, c.begin, [slots - 1, slots - 2], [slots - 3, slots - 4]))
+    assert torch.equal(o, o0) and torch.equal(far[slots - 3], past[2]) and torch.equal(far[slots - 4], past[3])
+
+
 # ------------------------------------------------------------------ norms
 
 GATED = [(1, 64, 64), (3, 48, 16), (7, 5120, 128), (5, 10240, 1280), (2, 960, 320), (4, 256, 256), (1, 32768, 32768),
