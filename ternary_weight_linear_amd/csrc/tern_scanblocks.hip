@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   uint16_t* y = a.y + (row0 * a.heads + head) * P;
   const float skip = a.d ? a.d[head] : 0.f;
   const int xown = place<8>(16 * upper + low, 2 * strip + (quarter >> 1)) + (quarter & 1) * 8;
-  f32x4 out;
-  float scale;  // exp(L) of the lane's row
-  auto store_y = [&](int t0, int turn) {  // of block t0
+  f32x4 out{0.f, 0.f, 0.f, 0.f};
+  float scale = 0.f;  // exp(L) of the lane's row
+  auto store_y = [&](const f32x4& out, float scale, int t0, int turn) {  // of block t0
     const f32x4 other = parts[turn][wave ^ 4][lane];
     float v[4];
 #pragma unroll
@@ -371,9 +371,8 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     const float factor = total;
     const uint2 x0 = transposed(xs[turn] + xt), x1 = transposed(xs[turn] + xt + 16 * 128);
     const u32x4 xf{x0.x, x0.y, x1.x, x1.y};  // x^T of the strip
-    if constexpr (!STATES) {
-      if (t0 > 0) store_y(t0 - kBlock, turn ^ 1);
-    }
+    const f32x4 before = out;
+    const float before_scale = scale;
     put(turn ^ 1);
     ask(t0 + 2 * kBlock);
     // ---- the half's part of y^T = S^T C^T, scaled; x^T M^T for the wave's rows
@@ -431,6 +430,7 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
       }
     }
     if constexpr (!STATES) {
+      if (t0 > 0) store_y(before, before_scale, t0 - kBlock, turn ^ 1);
       // A value of x that is not finite has reached the rows before it, through
       // zeros of M: the product is made again without it, and its column's results
       // from its row on are NaN.
@@ -439,15 +439,16 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
       for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, xf[i] & 0x7fff7fffu));
       if (__any(max((uint32_t)top.x, (uint32_t)top.y) >= 0x7f80u)) {
         u32x4 clean = xf;
-        int bad = kBlock;
+        int at = 8;  // the lane's first, in the order of its rows
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t w = xf[i >> 1] >> (16 * (i & 1));
           if ((w & 0x7f80u) == 0x7f80u) {
-            bad = min(bad, 16 * (i >> 2) + 4 * quarter + (i & 3));
+            at = min(at, i);
             clean[i >> 1] &= i & 1 ? 0xffffu : 0xffff0000u;
           }
         }
+        int bad = at == 8 ? kBlock : (at >> 2) * 16 + 4 * quarter + (at & 3);
         bad = min(bad, __shfl_xor(bad, 16));
         bad = min(bad, __shfl_xor(bad, 32));
         out = mfma(clean, mt, acc[0]);
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     turn = 1;
     if ((t0 += kBlock) >= last) break;
   }
-  if constexpr (!STATES) store_y(t0 - kBlock, turn);
+  if constexpr (!STATES) store_y(out, scale, t0 - kBlock, turn);
   if constexpr (STATES) {
     const int64_t to = state_at(unit, units, seg + 1) + strip;
     f32x4* p = (f32x4*)(ws + to * kWave) + upper * NB * 64 + lane;
