@@ -10,9 +10,9 @@
 // the lane and crosses lanes once a token.
 //
 // Measured (160 heads of 64 x 128): one token of 32 sequences 65 us, 5.2 TB/s of
-// states read and written, as a copy; 4 tokens of 16 sequences 41 us, 4.2 TB/s (each
-// further token costs about 3 us, its reduction and barrier); one token of one sequence
-// 5.2 us, the launch and three trips to memory.
+// states read and written, as a copy; 4 tokens of 16 sequences 39 us, 4.3 TB/s (each
+// further token costs about 2 us, its reduction and barrier); one token of one sequence
+// 4.9 us, the launch and three trips to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
