@@ -71,8 +71,9 @@ tern_status check_scan(const tern_state_batch* batch, int rows, int heads, int d
 constexpr int64_t kScanMaxStride = 1 << 22;  // elements: 64 rows stay below 2^30 bytes
 
 // Up to so many rows a sequence go token by token. Measured, token by token and in
-// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 49 and 52 us, with 12 rows 57 and 52; 64
-// sequences 150 and 156, 171 and 158; 2 of 40 heads of 128 x 256 with 12 rows 26 and 24.
+// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 46 and 52 us, with 12 rows 51 and 51,
+// with 16 59 and 52; 64 sequences 148 and 162, 158 and 163, 189 and 165; 2 of 40 heads of 128 x 256 21
+// and 23, 24.5 and 23.5, 30.5 and 23.5.
 constexpr int kScanStepRows = 8;
 
 // Segments of a prompt: as many as make the launches shortest, in microseconds as
