@@ -610,7 +610,9 @@ typedef struct {
  * x: [rows] of `channels`, x_stride elements apart, of `type`. weight
  * [channels][width] and bias [channels] (or NULL): of weight_type. y: bf16 rows
  * y_stride apart. width 2, 3 or 4; channels a multiple of 8 up to 2^20; pointers
- * and rows 16-byte aligned. y does not overlap x. Errors as tern_rmsnorm.
+ * and rows 16-byte aligned. y does not overlap x. A thread takes 16 rows of 16 bytes
+ * of channels of x: max_q rows are at most 2^31 threads, and those of all seqs, of
+ * each a multiple of 256, less than 2^32 (TERN_ERR_SHAPE). Errors as tern_rmsnorm.
  */
 tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void* x, tern_dtype type,
                              int64_t x_stride, int channels, int width, const void* weight, const void* bias,

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(256) tern_causal_conv_kernel(ConvArgs a) {
   constexpr int CH = kChannels<TYPE>, BYTES = 16 / CH;
   const int s = blockIdx.y;
   const int blocks = a.channels / CH;
-  const int at = blockIdx.x * 256 + threadIdx.x;
+  const int at = blockIdx.x * 256 + threadIdx.x;  // below 2^31, which the host sees to
   const int run = at / blocks, c0 = (at - run * blocks) * CH;
   const int t0 = run * kRun;
   // What does not depend on the batch's arrays is asked for before them: a single

@@ -43,7 +43,8 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
   a.x = x, a.w = weight, a.bias = bias, a.state = state, a.y = (uint16_t*)y_bf16;
   a.x_stride = x_stride, a.y_stride = y_stride;
   a.type = type, a.w_type = weight_type, a.channels = channels, a.width = width, a.slots = slots, a.silu = silu != 0;
-  if (tern::conv_blocks(a) > kMaxGrid)
+  // a thread's number within its sequence is an int in the kernel: 2^31 threads of 256 a workgroup
+  if (tern::conv_blocks(a) > kMaxGrid || tern::conv_blocks(a) / batch->seqs > (INT64_C(1) << 31) / 256)
     return fail(TERN_ERR_SHAPE, "tern_causal_conv: seqs * max_q * channels too large for one launch");
   const int err = tern::launch_conv(a, stream);
   if (err) return hip_fail(err, "causal_conv launch");
