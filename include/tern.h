@@ -641,6 +641,9 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
  * 32 rows, so a state that grows (D a > 0) leaves fp32 where that sum passes 88.
  * ws: device, tern_scan_workspace_bytes() bytes for the same arguments (16-byte
  * aligned, any contents; NULL if 0); calls that share it must not overlap.
+ * seqs * heads is below 2^24; in blocks, seqs times the tiles of 64 columns of the
+ * groups' heads below 2^23, and seqs times the blocks of max_q times the groups'
+ * heads by eight below 2^24 (TERN_ERR_SHAPE).
  * Errors as tern_rmsnorm, and TERN_ERR_WORKSPACE.
  */
 tern_status tern_scan(const tern_state_batch* batch, int rows, int heads, int dim, int groups, int state_dim,

@@ -53,6 +53,12 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
 
 namespace {
 
+// Up to so many rows a sequence go token by token. Measured, token by token and in
+// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 46 and 52 us, with 12 rows 51 and 51,
+// with 16 59 and 52; 64 sequences 148 and 162, 158 and 163, 189 and 165; 2 of 40 heads of 128 x 256 21
+// and 23, 24.5 and 23.5, 30.5 and 23.5.
+constexpr int kScanStepRows = 8;
+
 tern_status check_scan(const tern_state_batch* batch, int rows, int heads, int dim, int groups, int state_dim,
                        int slots, tern::ScanArgs* a) {
   if (tern_status st = check_states(batch, rows, slots, &a->batch)) return st;
@@ -63,19 +69,17 @@ tern_status check_scan(const tern_state_batch* batch, int rows, int heads, int d
   if (groups < 1 || heads % groups != 0)
     return fail(TERN_ERR_SHAPE, "groups=%d must divide heads=%d", groups, heads);
   a->heads = heads, a->dim = dim, a->groups = groups, a->state_dim = state_dim, a->slots = slots;
-  // a workgroup for every head, or for every 64 columns; segments are cut only where workgroups are few
-  if (2 * (int64_t)batch->seqs * heads > kMaxGrid || tern::scan_prepare_blocks(*a) > kMaxGrid)
+  // Token by token, workgroups of 256 threads, one a head; in blocks, of 512, one for
+  // every 64 columns of a group's heads (segments are cut only where those are few),
+  // behind a launch of 256. A grid's threads are counted in 32 bits.
+  const bool blocks = batch->max_q > kScanStepRows;
+  if (blocks ? 2 * tern::scan_units(*a) > kMaxGrid || tern::scan_prepare_blocks(*a) > kMaxGrid
+             : (int64_t)batch->seqs * heads > kMaxGrid)
     return fail(TERN_ERR_SHAPE, "tern_scan: seqs * heads or seqs * max_q * groups too large for one launch");
   return TERN_OK;
 }
 
 constexpr int64_t kScanMaxStride = 1 << 22;  // elements: 64 rows stay below 2^30 bytes
-
-// Up to so many rows a sequence go token by token. Measured, token by token and in
-// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 46 and 52 us, with 12 rows 51 and 51,
-// with 16 59 and 52; 64 sequences 148 and 162, 158 and 163, 189 and 165; 2 of 40 heads of 128 x 256 21
-// and 23, 24.5 and 23.5, 30.5 and 23.5.
-constexpr int kScanStepRows = 8;
 
 // Segments of a prompt: as many as make the launches shortest, in microseconds as
 // measured. A block of 32 tokens takes a workgroup 1.05 us in the last launch and
