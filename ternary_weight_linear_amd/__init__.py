@@ -642,6 +642,13 @@ def _int32(n, name):
         raise ValueError(f"{name}={n} does not fit 32 bits")
 
 
+def _fit(names, *sizes):
+    """_int32 for a tensor's sizes."""
+    if max(sizes) >= 2 ** 31:
+        for name, n in zip(names.split(), sizes):
+            _int32(n, name)
+
+
 def _on_gpu(t, name):
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
@@ -655,6 +662,7 @@ def _norm(x, weight, eps, residual, residual_out, q, scale, layout, y, stream, m
     if len(shape) != 2:
         raise ValueError(f"x must be [T, K], got {tuple(shape)}")
     T, K = shape
+    _fit("T K", T, K)
     xt, xs = _rows(x, "x", shape, device)
     wt, _ = _rows(weight, "weight", shape[1:], device)
     if not weight.is_contiguous():
@@ -752,6 +760,7 @@ class KVBatch:
         if page_table.dim() != 2:
             raise ValueError(f"page_table must be [seqs, width], got {tuple(page_table.shape)}")
         seqs, width = page_table.shape
+        _fit("seqs width", seqs, width)
         _dev(kv_len, torch.int32, "kv_len", (seqs,), page_table.device)
         _dev(q_begin, torch.int32, "q_begin", (seqs + 1,), page_table.device)
         self.q_begin, self.kv_len, self.page_table = q_begin, kv_len, page_table
@@ -774,6 +783,7 @@ class Rope:
         _dev(table, torch.float32, "table")
         if table.dim() != 3 or table.shape[2] != 2:
             raise ValueError(f"table must be [positions, pairs, 2], got {tuple(table.shape)}")
+        _fit("positions pairs", *table.shape[:2])
         if axis is None:
             axis = torch.zeros((table.shape[1],), dtype=torch.uint8, device=table.device)
         _dev(axis, torch.uint8, "axis", (table.shape[1],), table.device)
@@ -784,6 +794,7 @@ class Rope:
         """The C struct for positions of so many axes (made once for each)."""
         r = self._refs.get(axes)
         if r is None:
+            _int32(axes, "axes")
             r = self._refs[axes] = ctypes.byref(_Rope(self.table.data_ptr(), self.axis.data_ptr(), self.table.shape[1],
                                                       self.table.shape[0], axes))
         return r
@@ -955,6 +966,7 @@ class StateBatch:
         if src.dim() != 1:
             raise ValueError(f"src must be [seqs], got {tuple(src.shape)}")
         seqs = src.shape[0]
+        _int32(seqs, "seqs")
         _dev(dst, torch.int32, "dst", (seqs,), src.device)
         _dev(begin, torch.int32, "begin", (seqs + 1,), src.device)
         _int32(max_q, "max_q")
@@ -1011,9 +1023,13 @@ def causal_conv(x, weight, state, batch: StateBatch, bias=None, activation="silu
     if len(shape) != 2:
         raise ValueError(f"x must be [rows, channels], got {tuple(shape)}")
     rows, channels = shape
-    xt, xs = _rows(x, "x", shape, device)
     if weight.dim() != 2:
         raise ValueError(f"weight must be [channels, width], got {tuple(weight.shape)}")
+    if state.dim() != 3:
+        raise ValueError(f"state must be [slots, width - 1, channels], got {tuple(state.shape)}")
+    slots = state.shape[0]
+    _fit("rows channels slots", rows, channels, slots)
+    xt, xs = _rows(x, "x", shape, device)
     width = weight.shape[1]
     wt = _whole(weight, "weight", (channels, width), device)
     bp = None
@@ -1021,9 +1037,6 @@ def causal_conv(x, weight, state, batch: StateBatch, bias=None, activation="silu
         if _whole(bias, "bias", (channels,), device) != wt:
             raise TypeError("bias must have the weight's type")
         bp = bias.data_ptr()
-    if state.dim() != 3:
-        raise ValueError(f"state must be [slots, width - 1, channels], got {tuple(state.shape)}")
-    slots = state.shape[0]
     if _whole(state, "state", (slots, width - 1, channels), device) != xt:
         raise TypeError("state must have the type of x")
     if activation not in _ACTIVATIONS:
@@ -1074,10 +1087,12 @@ def scan(x, b, c, dt, a, state, batch: StateBatch, d=None, dt_bias=None, softplu
     if len(shape) != 3:
         raise ValueError(f"x must be [rows, heads, dim], got {tuple(shape)}")
     rows, heads, dim = shape
-    xs = _bf16_rows(x, "x", shape, device)
     if b.dim() != 3:
         raise ValueError(f"b must be [rows, groups, state_dim], got {tuple(b.shape)}")
     groups, n = b.shape[1:]
+    slots = state.shape[0] if state.dim() == 4 else -1
+    _fit("rows heads dim groups state_dim slots", rows, heads, dim, groups, n, slots)
+    xs = _bf16_rows(x, "x", shape, device)
     shared = (rows, groups, n)
     bs = _bf16_rows(b, "b", shared, device)
     cs = _bf16_rows(c, "c", shared, device)
@@ -1091,7 +1106,6 @@ def scan(x, b, c, dt, a, state, batch: StateBatch, d=None, dt_bias=None, softplu
     if dt_bias is not None:
         _f32(dt_bias, "dt_bias", each, device)
         bp = dt_bias.data_ptr()
-    slots = state.shape[0] if state.dim() == 4 else -1
     _f32(state, "state", (slots, heads, n, dim), device)
     _on_device(batch, "batch", device)
     if out is None:
@@ -1130,18 +1144,23 @@ def _matrix(x):
     device, shape = _on_gpu(x, "x"), x.shape
     if len(shape) != 2:
         raise ValueError(f"x must be [T, K], got {tuple(shape)}")
+    _fit("T K", *shape)
     return device, shape
 
 
 def _gated(x, z, weight, eps, group, gate_first, q, scale, layout, y, stream, made):
     device, shape = _matrix(x)
     T, K = shape
+    if group is None:
+        group = K
+    else:
+        _int32(group, "group")
     xt, xs = _rows(x, "x", shape, device)
     zt, zs = _rows(z, "z", shape, device)
     wt = _whole(weight, "weight", shape[1:], device)
     qp, sp, yp, ys = _norm_outputs(shape, device, q, scale, y, made)
     _check(lib().tern_rmsnorm_gated(x.data_ptr(), xt, xs, z.data_ptr(), zt, zs, weight.data_ptr(), wt,
-                                    K if group is None else group, int(gate_first), eps, T, K, qp, sp, Q_LAYOUTS[layout],
+                                    group, int(gate_first), eps, T, K, qp, sp, Q_LAYOUTS[layout],
                                     yp, ys, _stream(stream)))
 
 
