@@ -336,7 +336,7 @@ inline int64_t scan_prepared_bytes(const ScanArgs& a) {
   return ((int64_t)a.batch.rows / kScanBlock + a.batch.seqs + 1) * a.heads * kScanHeadBytes;
 }
 inline int64_t scan_ws_bytes(const ScanArgs& a, const ScanPlan& p) {
-  return scan_prepared_bytes(a) + (p.segments == 1 ? 0 : scan_units(a) * p.segments * 4 * ((int64_t)a.state_dim * 16 + 1) * 4);
+  return scan_prepared_bytes(a) + (p.segments == 1 ? 0 : scan_units(a) * p.segments * 4 * ((int64_t)a.state_dim * 16 + 2) * 4);
 }
 TERN_WEAK int launch_scan_blocks(const ScanArgs& a, const ScanPlan& p, void* ws, void* stream);
 

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint
 
 // Where the state at the start of segment j of a unit lies, for strip 0 of it: states in
 // the order of the registers, [N / 16][lane] times four, behind them one decay a strip,
-// that of the segment before.
+// that of the segment before, as a fraction and a power of two.
 __device__ __forceinline__ int64_t state_at(int unit, int units, int j) { return ((int64_t)j * units + unit) * 4; }
 
 template <int P, int N, bool STATES>
@@ -325,7 +325,10 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
       }
     }
   }
-  float decay = 1.f;
+  // The segment's decay, fraction 2^power: where states grow, the product of its blocks'
+  // factors may leave fp32 though none of them does and no state.
+  float fraction = 1.f;
+  int power = 0;
 
   // ---- what a lane reads of the tiles; the rest of an address is constant
   const int tr = 4 * quarter + (lane >> 2 & 3), piece = lane & 3;  // transposed: row, 4 columns
@@ -403,7 +406,11 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     }
     if constexpr (LATE) put(turn ^ 1), ask(t0 + 2 * kBlock);
     // ---- the next state
-    decay *= factor;
+    if constexpr (STATES) {
+      fraction *= __builtin_amdgcn_frexp_mantf(factor);
+      power += __builtin_amdgcn_frexp_expf(factor) + __builtin_amdgcn_frexp_expf(fraction);
+      fraction = __builtin_amdgcn_frexp_mantf(fraction);
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -483,7 +490,8 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     f32x4* p = (f32x4*)(ws + to * kWave) + upper * NB * 64 + lane;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) p[nb * 64] = S[nb];
-    if (lane == 0 && !upper) ws[state_at(0, units, plan.segments) * kWave + to] = decay;
+    if (lane == 0 && !upper)
+      *(float2*)(ws + state_at(0, units, plan.segments) * kWave + 2 * to) = float2{fraction, __int_as_float(power)};
   } else {
     const int dst = a.batch.dst[s];
     if (ends && live && dst >= 0 && dst < a.slots) {
@@ -522,13 +530,13 @@ __global__ void __launch_bounds__(256) tern_scan_join_kernel(ScanArgs a, ScanPla
 #pragma unroll
     for (int r = 0; r < 4; ++r) S[r] = p[r * P];
   }
-  const float* decays = ws + state_at(0, units, plan.segments) * kWave;
+  const float2* decays = (const float2*)(ws + state_at(0, units, plan.segments) * kWave);
   f32x4* at = (f32x4*)(ws + (state_at(unit, units, 0) + wave) * kWave) + nb * 64 + lane;
   const int64_t step = (int64_t)units * kWave;  // of four floats: a segment
   at[0] = S;
   for (int j0 = 1; j0 <= count; j0 += AT_ONCE) {
     f32x4 v[AT_ONCE];
-    float decay[AT_ONCE];
+    float2 decay[AT_ONCE];
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i) {
       const int j = min(j0 + i, count);
@@ -538,7 +546,7 @@ __global__ void __launch_bounds__(256) tern_scan_join_kernel(ScanArgs a, ScanPla
     for (int i = 0; i < AT_ONCE; ++i) {
       if (j0 + i > count) break;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[r] = __builtin_fmaf(decay[i], S[r], v[i][r]);
+      for (int r = 0; r < 4; ++r) S[r] = __builtin_ldexpf(S[r] * decay[i].x, __float_as_int(decay[i].y)) + v[i][r];
       at[(j0 + i) * step] = S;
     }
   }
