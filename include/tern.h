@@ -635,8 +635,8 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
  * States are fp32 throughout. Calls with max_q of more than 8 rows work in
  * blocks of 32 rows through matrix products of bf16 operands with fp32 sums: B, C
  * and x enter as they are, weighted x enters the next state with all of its 24
- * bits; the weights inside a block and, for y only, the state before it are rounded
- * to bf16. There, a value that is not finite makes the results that depend on it
+ * bits; the weights inside a block and, for y only, the state before it enter as two
+ * bf16 numbers each, off by at most 2^-15 of themselves. There, a value that is not finite makes the results that depend on it
  * infinite or NaN; no other rows or channels. A block takes exp() of D a summed over up to
  * 32 rows, so a state that grows (D a > 0) leaves fp32 where that sum passes 88.
  * ws: device, tern_scan_workspace_bytes() bytes for the same arguments (16-byte

@@ -19,9 +19,11 @@
 // operand's lanes, C in LDS in the order of k. B and x are read transposed from LDS.
 //
 // Sums, states and the factors exp() are fp32. B, C and x are bf16 as given. M and
-// S enter y's products rounded to bf16, which is what y itself is rounded to; the
-// weighted x enters the next state, which is kept in fp32, as three bf16 numbers
-// that hold all of its 24 bits.
+// S enter y's products as two bf16 numbers each, which hold them to 2^-15, and the
+// weighted x enters the next state, whose errors add up over a sequence, as three, which
+// hold all of its 24 bits. (With one number each for M and S y is off by 2^-8 of its terms,
+// as much as its own rounding where they do not cancel, and more where they do; 2048 tokens
+// of 160 heads took 83 us.)
 //
 // Few workgroups (one sequence, few heads): the tokens of a sequence are cut
 // into segments. A launch computes each segment's own state from zeros and its
@@ -68,6 +70,14 @@ __device__ __forceinline__ uint2 transposed(const uint8_t* p) {
   return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
 }
 
+// a and b as two bf16 numbers each, to 2^-15: their upper halves, and what those leave, rounded.
+// (An instruction that rounds a pair takes twice the time of one that picks halves: with the
+// upper ones rounded too, to 2^-16, 2048 tokens of 160 heads take 95.0 us and not 92.6.)
+__device__ __forceinline__ void split2(float a, float b, uint32_t& upper, uint32_t& lower) {
+  upper = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  lower = pack_bf16(a - bf16_hi(__float_as_uint(a)), b - bf16_hi(__float_as_uint(b)));
+}
+
 // v exactly, as three numbers of 8 bits: what its upper half holds, what the
 // upper half of the rest holds, and the rest.
 __device__ __forceinline__ void split3(const float (&v)[8], u32x4 (&part)[3]) {
@@ -102,10 +112,12 @@ __device__ __forceinline__ float sums_down(float v, int lane) {
   return v + (lane & 16 ? 0.f : lane & 32 ? b : a);
 }
 
-// What the first launch leaves for a block of a head: M^T, 2 KB in the order of
-// two operands' lanes, then exp(L) and exp(L[31] - L) D of its tokens.
-constexpr int kHeadBytes = kScanHeadBytes;
-static_assert(kHeadBytes == 2048 + 2 * kBlock * 4, "layout of a head's block");
+// What the first launch leaves for a block of a head, in the order of operands' lanes, 1 KB
+// each: M^T of the rows s < 16, whose t < 16 alone are not zero: the bf16 numbers in the
+// first half of k, what they leave in the second; M^T of the other rows; what that
+// leaves. Then exp(L) and exp(L[31] - L) D of its tokens.
+constexpr int kHeadBytes = kScanHeadBytes, kFactors = 3072;
+static_assert(kHeadBytes == kFactors + 2 * kBlock * 4, "layout of a head's block");
 
 // Place of a block in the workspace: blocks of a sequence start at its rows
 // begin + 32 i, so row / 32 + s differs for all of them.
@@ -113,7 +125,7 @@ __device__ __forceinline__ int64_t block_at(int64_t row, int s) { return (row >>
 
 // M and factors: a workgroup takes a block of a sequence and eight heads of a
 // group, two a wave. Its first three waves make C B^T, 16 x 16 blocks each. Bound
-// by the chain of loads, sums and products of each workgroup, then by writing M, 2 KB a
+// by the chain of loads, sums and products of each workgroup, then by writing M, 3 KB a
 // head and block.
 template <int N>
 __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint8_t* ws) {
@@ -160,7 +172,7 @@ __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint
   const float behind = low == 31 ? 0.f : next;
   shared[wave][half][0][low] = L, shared[wave][half][1][low] = D;
   if (h0 + half < hpg) {
-    float* to = (float*)(ws + (block_at(row0, s) * a.heads + h) * kHeadBytes + 2048) + low;
+    float* to = (float*)(ws + (block_at(row0, s) * a.heads + h) * kHeadBytes + kFactors) + low;
     to[0] = __builtin_amdgcn_exp2f(L), to[kBlock] = D * __builtin_amdgcn_exp2f(behind);
   }
   __syncthreads();
@@ -171,7 +183,7 @@ __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint
     const float(&Ls)[kBlock] = shared[wave][i][0];
     const float(&Ds)[kBlock] = shared[wave][i][1];
     const float own[2] = {Ls[low16], Ls[16 + low16]};
-    uint2 out[3];
+    uint2 out[3], left[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       const int t = j == 2 ? 16 : 0;
@@ -182,10 +194,12 @@ __global__ void __launch_bounds__(256) tern_scan_prepare_kernel(ScanArgs a, uint
         m[k] = cb[k] * (__builtin_amdgcn_exp2f(own[j > 0] - ft[k]) * fd[k]);
         if (j != 1) m[k] = over < k ? 0.f : m[k];
       }
-      out[j] = uint2{pack_bf16(m[0], m[1]), pack_bf16(m[2], m[3])};
+      split2(m[0], m[1], out[j].x, left[j].x), split2(m[2], m[3], out[j].y, left[j].y);
     }
     u32x4* to = (u32x4*)(ws + (block_at(row0, s) * a.heads + g * hpg + h0 + i) * kHeadBytes) + lane;
-    to[0] = u32x4{out[0].x, out[0].y, 0, 0}, to[64] = u32x4{out[1].x, out[1].y, out[2].x, out[2].y};
+    to[0] = u32x4{out[0].x, out[0].y, left[0].x, left[0].y};
+    to[64] = u32x4{out[1].x, out[1].y, out[2].x, out[2].y};
+    to[128] = u32x4{left[1].x, left[1].y, left[2].x, left[2].y};
   }
 }
 
@@ -249,9 +263,17 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   const uint8_t* from = prepared + (block_at(row0, s) * a.heads + head) * kHeadBytes;
   const int64_t next = (int64_t)a.heads * kHeadBytes;
   struct {  // the block on its way
-    u32x4 x, b[BL], c[STATES ? 1 : BL], m;
+    u32x4 x, b[BL], c[STATES ? 1 : BL];
     float f;
   } ahead;
+  u32x4 m, m_left;  // M^T of the wave's rows s, of the block worked on next
+  const int moff = 1024 * upper + 16 * lane, mleft = upper ? 2048 + 16 * lane : kOffPastEnd;
+  const uint8_t* from_m = from;
+  auto ask_m = [&](bool in) {
+    const rsrc_t pres = make_rsrc(from_m, in ? kHeadBytes : 0);
+    m = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(pres, moff, 0, 0));
+    m_left = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(pres, mleft, 0, 0));
+  };
   // Behind the last block every load is past the end, and costs nothing.
   auto ask = [&](int t0) {
     const int n = min(last - t0, kBlock) - 1;
@@ -263,13 +285,12 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
 #pragma unroll
     for (int i = 0; i < BL; ++i)
       ahead.b[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(bres, boff + BR * i * bstep, 0, 0));
-    ahead.f = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(pres, 2048 + 4 * lane, 0, 0));
+    ahead.f = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(pres, kFactors + 4 * lane, 0, 0));
     if constexpr (!STATES) {
       const rsrc_t cres = make_rsrc(c, in ? n * cstep + 2 * N : 0);
 #pragma unroll
       for (int i = 0; i < BL; ++i)
         ahead.c[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(cres, coff + BR * i * cstep, 0, 0));
-      ahead.m = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(pres, 1024 * upper + 16 * lane, 0, 0));
       c += kBlock * a.c_stride;
     }
     x += kBlock * a.x_stride, b += kBlock * a.b_stride, from += next;
@@ -279,8 +300,7 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   const int xput = place<8>(tid / 8, tid % 8), bput = place<CH>(brow, bch);
   const int cput = place<CH>(brow, (bch & ~3) + (bch & 1) * 2) + (bch >> 1 & 1) * 8;
   const int cput1 = place<CH>(brow, (bch & ~3) + (bch & 1) * 2 + 1) + (bch >> 1 & 1) * 8;
-  u32x4 m;  // M^T of the wave's rows s and the decay of the block whose tiles were put last
-  float total;
+  float total;  // the decay of the block whose tiles were put last
   auto put = [&](int turn) {
     if (copies_x) *(u32x4*)(xs[turn] + xput) = ahead.x;
     if (copies_b) {
@@ -295,9 +315,9 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     }
     fs[turn][wave][lane] = ahead.f;
     total = of_lane(ahead.f, 31);
-    if constexpr (!STATES) m = ahead.m;
   };
   ask(0);
+  if constexpr (!STATES) ask_m(true);
 
   // ---- the state at the segment's start: register r of block nb holds row
   // 16 nb + 4 quarter + r of the wave's half
@@ -366,35 +386,35 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(i32x2, *(const uint2*)yget), yres, yoff, 0, 0);
   };
 
-  // The next block's copies stand in the way of this one's operands, unless a block has so
-  // little to do that its loads would not be back: 2048 tokens of 160 heads of 64 x 128
-  // take 73.2 us with late copies and 74.7 with early ones, 3 x 509 of 40 heads of 128 x 64 20.5 and 18.5.
-  constexpr bool LATE = N > 64;
   // Block t0, whose tiles lie in buffer `turn`. The next one's go into the other
   // buffer, which was read before the last barrier.
   auto step = [&](auto constant, int t0) {
     constexpr int turn = decltype(constant)::value;
-    const u32x4 mt = m;
     const float factor = total;
     const uint2 x0 = transposed(xs[turn] + xt), x1 = transposed(xs[turn] + xt + 16 * 128);
     const u32x4 xf{x0.x, x0.y, x1.x, x1.y};  // x^T of the strip
     const f32x4 before = out;
     const float before_scale = scale;
-    if constexpr (!LATE) put(turn ^ 1), ask(t0 + 2 * kBlock);
     // ---- the half's part of y^T = S^T C^T, scaled; x^T M^T for the wave's rows
     f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     if constexpr (!STATES) {
+      u32x4 high[KQ], lower[KQ];
 #pragma unroll
-      for (int q = 0; q < KQ; ++q) {
-        u32x4 v;
+      for (int q = 0; q < KQ; ++q)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          v[2 * j] = pack_bf16(S[2 * q + j][0], S[2 * q + j][1]);
-          v[2 * j + 1] = pack_bf16(S[2 * q + j][2], S[2 * q + j][3]);
+        for (int j = 0; j < 4; ++j) {
+          uint32_t h, l;
+          split2(S[2 * q + (j >> 1)][2 * (j & 1)], S[2 * q + (j >> 1)][2 * (j & 1) + 1], h, l);
+          high[q][j] = h, lower[q][j] = l;
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j] = mfma(v, *(const u32x4*)(cs[turn] + co[j][q & 1] + (q >> 1) * 128), acc[j]);
-      }
+      for (int q = 0; q < KQ; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const u32x4 ct = *(const u32x4*)(cs[turn] + co[j][q & 1] + (q >> 1) * 128);
+          acc[j] = mfma(high[q], ct, acc[j]);
+          acc[j] = mfma(lower[q], ct, acc[j]);
+        }
       parts[turn][wave][lane] = acc[1];
       scale = fs[turn][wave][16 * upper + low];
       const uint2 own = *(const uint2*)(xs[turn] + xown);
@@ -402,9 +422,15 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
       for (int r = 0; r < 4; ++r) acc[0][r] *= scale;
       acc[0][0] = __builtin_fmaf(skip, bf16_lo(own.x), acc[0][0]), acc[0][1] = __builtin_fmaf(skip, bf16_hi(own.x), acc[0][1]);
       acc[0][2] = __builtin_fmaf(skip, bf16_lo(own.y), acc[0][2]), acc[0][3] = __builtin_fmaf(skip, bf16_hi(own.y), acc[0][3]);
-      out = mfma(xf, mt, acc[0]);
+      // the rows s < 16 meet the rows t < 16 twice, with M and with what it left
+      out = mfma(xf, m_left, mfma(upper ? xf : u32x4{xf[0], xf[1], xf[0], xf[1]}, m, acc[0]));
+      from_m += next;
+      ask_m(t0 + kBlock < last);
     }
-    if constexpr (LATE) put(turn ^ 1), ask(t0 + 2 * kBlock);
+    // The next block's copies wait until this one's operands of y are read: in front of them they
+    // take 151 and not 144 us of 2048 tokens of 160 heads of 128 x 128, 145 and 141 of 64 x 256, 96 and 95
+    // of 64 x 128; 81.0 and 81.2 of 64 x 64, and a microsecond less where a call has 16 blocks.
+    put(turn ^ 1), ask(t0 + 2 * kBlock);
     // ---- the next state
     if constexpr (STATES) {
       fraction *= __builtin_amdgcn_frexp_mantf(factor);
@@ -462,7 +488,11 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
         int bad = at == 8 ? kBlock : (at >> 2) * 16 + 4 * quarter + (at & 3);
         bad = min(bad, __shfl_xor(bad, 16));
         bad = min(bad, __shfl_xor(bad, 32));
-        out = mfma(clean, mt, acc[0]);
+        from_m -= next;
+        ask_m(true);
+        out = mfma(clean, m_left, mfma(upper ? clean : u32x4{clean[0], clean[1], clean[0], clean[1]}, m, acc[0]));
+        from_m += next;
+        ask_m(t0 + kBlock < last);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int since = __shfl(bad, 4 * quarter + r);
