@@ -54,9 +54,9 @@ tern_status tern_causal_conv(const tern_state_batch* batch, int rows, const void
 namespace {
 
 // Up to so many rows a sequence go token by token. Measured, token by token and in
-// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 46 and 52 us, with 12 rows 51 and 51,
-// with 16 59 and 52; 64 sequences 148 and 162, 158 and 163, 189 and 165; 2 of 40 heads of 128 x 256 21
-// and 23, 24.5 and 23.5, 30.5 and 23.5.
+// blocks: 16 sequences of 160 heads of 64 x 128 with 8 rows 46 and 56 us, with 12 rows 52 and 57,
+// with 16 59 and 57; 64 sequences 137 and 180, 166 and 181, 196 and 183; 2 of 40 heads of 128 x 256 22
+// and 25, 25 and 24, 30 and 24.
 constexpr int kScanStepRows = 8;
 
 tern_status check_scan(const tern_state_batch* batch, int rows, int heads, int dim, int groups, int state_dim,
@@ -81,21 +81,31 @@ tern_status check_scan(const tern_state_batch* batch, int rows, int heads, int d
 
 constexpr int64_t kScanMaxStride = 1 << 22;  // elements: 64 rows stay below 2^30 bytes
 
-// Segments of a prompt: as many as make the launches shortest, in microseconds as
-// measured. A block of 32 tokens takes a workgroup 1.05 us in the last launch and
-// 0.75 us in the one before it, which only S > 1 segments need, while a compute
-// unit has one, and that much longer the more it has; two launches more cost 15 us. Measured, in all
-// (64 blocks, 160 units): 87, 111, 95, 100 and 105 us for 1, 2, 3, 4 and 6
-// segments; 256 blocks of 20 units: 261, 123, 74, 63, 59 and 64 us for 1, 4, 8, 11, 22 and 32.
+// Segments of a prompt: as many as make the launches shortest, in microseconds as measured.
+// A block of 32 tokens takes a workgroup alone on its compute unit `last` in the last
+// launch and `before` in the one before it, which only several segments need; k
+// workgroups on a unit take about 0.85 k times as long (two 1.55 to 1.9, three 2.5); two
+// launches more cost 16, and the segments' states cross the memory four times, 256
+// bytes a row of state each. Measured with so many segments, those taken here in brackets:
+//   64 blocks of 160 units of 64 x 128: [1] 95, 2 121, 3 103, 4 109 us;
+//   256 blocks of 20 units of 64 x 128: 1 299, 4 131, 8 79, 11 67, [12] 63, 16 70, 24 61, 32 67;
+//   of 64 x 64: 1 225, 8 62, 11 54, 12 51, 16 57, [24] 49; of 64 x 256: 1 440, 8 109, 11 94, [12] 88, 16 110, 24 97;
+//   64 blocks of 40 units of 64 x 128: 1 84, 3 59, 4 50, [6] 44, 8 48, 16 51;
+//   128 blocks of 80 units of 64 x 128: 1 165, 3 117, 4 122, [6] 104, 8 118, 16 126.
 tern::ScanPlan plan_scan(const tern::ScanArgs& a) {
   const int64_t blocks = (a.batch.max_q + tern::kScanBlock - 1) / tern::kScanBlock, units = tern::scan_units(a);
+  const double last = a.state_dim == 64 ? 0.85 : a.state_dim == 128 ? 1.13 : 1.68;
+  const double before = a.state_dim == 64 ? 0.51 : a.state_dim == 128 ? 0.67 : 0.82;
+  const auto shared = [](int64_t workgroups) {
+    const int64_t k = (workgroups + kComputeUnits - 1) / kComputeUnits;
+    return k <= 1 ? 1.0 : 0.85 * (double)k;
+  };
   tern::ScanPlan p{1, (int)blocks * tern::kScanBlock};
   double least = 0;
   for (int64_t s = 1; s <= std::min<int64_t>(64, blocks / 4 + 1) && (s == 1 || units < kComputeUnits); ++s) {
     const int64_t length = (blocks + s - 1) / s, used = (blocks + length - 1) / length;
-    const double each = 1.05 * std::max(1.0, (double)(units * used) / kComputeUnits);
-    const double before = used == 1 ? 0 : 0.75 * std::max(1.0, 1.1 * (double)(units * (used - 1)) / kComputeUnits);
-    const double us = length * (each + before) + (used == 1 ? 0 : 15);
+    double us = length * last * shared(units * used);
+    if (used > 1) us += length * before * shared(units * (used - 1)) + 16 + 2e-4 * (double)(units * used * a.state_dim);
     if (s == 1 || us < least) {
       least = us;
       p.length = (int)length * tern::kScanBlock, p.segments = (int)used;
