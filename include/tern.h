@@ -591,7 +591,9 @@ size_t tern_kv_attn_workspace_bytes(const tern_kv_cache* cache, const tern_kv_ba
  * max_q bounds the rows of a sequence. src and dst may be the same slot. A slot
  * that one sequence writes must not be read or written by another sequence of
  * the call. A sequence without rows, or whose begin leaves the rows of the call
- * or exceeds max_q, is left out: its rows and its slot are not written.
+ * or exceeds max_q, is left out: its rows and its slot are not written. A row belongs to
+ * one sequence: where begin falls and two sequences have rows in common, their results
+ * and states are unspecified (no access leaves the buffers).
  */
 typedef struct {
   const int32_t* begin;

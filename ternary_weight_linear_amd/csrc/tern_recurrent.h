@@ -21,8 +21,9 @@ __device__ __forceinline__ float exp_of(float x) {
 }
 
 // z / (1 + exp(-z)), to about 6 + |z| / 4 roundings: the rounding of the exponent
-// -z log2(e) is put back to first order, that of the constant is not. 0 from -88
-// down, where the value is below 2^-120.
+// -z log2(e) is put back to first order, that of the constant is not. 0 from -87.33
+// down, where exp(-z) passes 2^126 and its reciprocal the normal range; the value is below
+// 2^-119 there.
 __device__ __forceinline__ float silu(float z) {
   constexpr float kLog2e = -0x1.715476p+0f;
   const float c = __builtin_amdgcn_fmed3f(z, -126.f, 126.f), t = c * kLog2e;
