@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   f32x4 S[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) S[nb] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t mine = ((int64_t)head * N + upper * (N / 2) + 4 * quarter) * P + column + low;
+  const int64_t mine = ((int64_t)head * N + upper * (N / 2)) * P + column;  // of the wave
   const int64_t slot = (int64_t)a.heads * N * P;
   constexpr int64_t kWave = N * 16;
   if constexpr (!STATES) {
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
     } else {
       const int src = a.batch.src[s];
       if (src >= 0 && src < a.slots) {
-        const float* p = a.state + src * slot + mine;
+        const float* p = a.state + src * slot + mine + 4 * quarter * P + low;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(512, N == 256 ? 2 : 4) tern_scan_blocks_kernel
   } else {
     const int dst = a.batch.dst[s];
     if (ends && live && dst >= 0 && dst < a.slots) {
-      float* p = a.state + dst * slot + mine;
+      // the lane's number anew: kept, its place would be in memory through the loop
+      const int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+      float* p = a.state + dst * slot + mine + 4 * (l >> 4) * P + (l & 15);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
