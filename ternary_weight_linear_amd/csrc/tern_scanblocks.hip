@@ -29,14 +29,14 @@
 // into segments. A launch computes each segment's own state from zeros and its
 // decay, the next puts the states at the segments' starts together in order.
 //
-// Bound by the issue of each workgroup's chain through a block (about 1.15 us for 64
-// columns x 128 rows of state: loads to LDS, products, rounding, a barrier), which
+// Bound by the issue of each workgroup's chain through a block (about 1.27 us for 64
+// columns x 128 rows: loads to LDS, products, rounding, a barrier), which
 // few workgroups cannot hide; the matrix cores and HBM are far from full. Measured:
-// 2048 tokens of 160 heads of 64 x 128 in 12 + 74 us (11 us of matrix products at the whole
-// chip's rate, 21 us of traffic); 3 x 509 of 40 heads of 128 x 64 in 5 + 19; 8192 of 20
-// heads of 64 x 128 in 11 segments, 8 + 21 + 6 + 33. Products of 32 x 32 x 16 with 128
-// columns a workgroup take 65 us against 82 here for 512 tokens of 1024 heads, and are
-// slower where units are few.
+// 2048 tokens of 160 heads of 64 x 128 in 15 + 82 us (13 us of matrix products at the whole
+// chip's rate, 21 us of traffic); 3 x 509 of 40 heads of 128 x 64 in 5 + 20; 8192 of 20
+// heads of 64 x 128 in 12 segments, 9 + 19 + 6 + 33. Products of 32 x 32 x 16 with 128
+// columns a workgroup (with one number each for M and S) took 65 us against 82 for 512 tokens of
+// 1024 heads, and were slower where units are few.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
