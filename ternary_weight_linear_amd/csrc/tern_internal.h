@@ -322,7 +322,7 @@ struct ScanPlan {
   int segments, length;
 };
 constexpr int kScanBlock = 32;
-constexpr int kScanHeadBytes = 3072 + 2 * kScanBlock * 4;  // prepared for a head and block
+constexpr int kScanHeadBytes = 3 * 1024 + 2 * kScanBlock * 4;  // prepared for a head and block
 inline int64_t scan_units(const ScanArgs& a) {
   return ((int64_t)a.heads / a.groups * a.dim + 63) / 64 * a.groups * a.batch.seqs;
 }

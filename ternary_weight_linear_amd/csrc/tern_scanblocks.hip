@@ -116,7 +116,7 @@ __device__ __forceinline__ float sums_down(float v, int lane) {
 // each: M^T of the rows s < 16, whose t < 16 alone are not zero: the bf16 numbers in the
 // first half of k, what they leave in the second; M^T of the other rows; what that
 // leaves. Then exp(L) and exp(L[31] - L) D of its tokens.
-constexpr int kHeadBytes = kScanHeadBytes, kFactors = 3072;
+constexpr int kHeadBytes = kScanHeadBytes, kFactors = 3 * 1024;
 static_assert(kHeadBytes == kFactors + 2 * kBlock * 4, "layout of a head's block");
 
 // Place of a block in the workspace: blocks of a sequence start at its rows
